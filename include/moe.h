@@ -284,6 +284,108 @@ typedef struct {
 moe_status moe_compute_load_stats(const moe_config* cfg, const int32_t* counts, const int32_t* offsets,
                                   moe_load_stats* stats, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The layer in 8 bits: e4m3 operands (4 exponent and 3 mantissa bits, largest
+ * value 448, one byte each) with one fp32 scale per block, as DeepSeek-V3-style
+ * layers are served.  A block is 128 columns of one row for activations and
+ * 128 x 128 for weights; the last block of an axis may be shorter.
+ *   scale = max(fl32(amax / 448), 2^-126),  code = e4m3(x * fl32(1 / scale)),
+ * rounded to nearest even, saturated.  A NaN gives a NaN code (and does not
+ * enter amax); a block with an infinity gives NaN products.
+ * Scales of a row-blocked [R][K] matrix are [R][ceil(K / 128)], those of
+ * weights [G][N][K] are [G][ceil(N / 128)][ceil(K / 128)].  Any positive scales
+ * are taken as they are: they need not come from moe_quantize_fp8.
+ * Products: K % 16 == 0 and 16-byte aligned code pointers (TMA), else
+ * MOE_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+
+/* The layer's weights with e4m3 expert matrices (same shapes as moe_weights). */
+typedef struct {
+  const void* norm_w;             /* [d]     act dtype */
+  const void* w_router;           /* [E][d]  act dtype: the router is not quantised */
+  const void* w_gate;             /* [E][H][d] e4m3 */
+  const float* w_gate_scale;      /* [E][ceil(H/128)][ceil(d/128)] */
+  const void* w_up;               /* [E][H][d] e4m3 */
+  const float* w_up_scale;
+  const void* w_down;             /* [E][d][H] e4m3 */
+  const float* w_down_scale;      /* [E][ceil(d/128)][ceil(H/128)] */
+  const void* ws_gate;            /* shared expert (NULL when Hs = 0), as above without [E] */
+  const float* ws_gate_scale;
+  const void* ws_up;
+  const float* ws_up_scale;
+  const void* ws_down;
+  const float* ws_down_scale;
+} moe_weights_fp8;
+
+/* Residual add, RMSNorm (step a1) and quantisation in one pass over the rows:
+ *   s = act(x + residual),  v = fl32(fl32(s * r) * w),  r = fl32(1/sqrt(mean(s^2) + eps)), mean in fp64,
+ *   xn = act(v),  (q, q_scale) = v in e4m3, one scale per 128 columns (from the unrounded fp32 v).
+ * xn has the bits that moe_route gives for h = s.
+ *   x [N][d], residual [N][d] or NULL (s = x), norm_w [d];
+ *   outputs, each NULL if not wanted: res_out [N][d] = s (may equal x or
+ *   residual), xn [N][d] (may equal x or residual, not res_out), q [N][d] with
+ *   q_scale [N][ceil(d/128)] (both or neither).
+ * Any d up to 49152, odd ones included; cfg gives N, d, dtype and rms_eps.
+ * MOE_ERR_INVALID_ARG when no output is wanted or only one of q, q_scale. */
+moe_status moe_add_rmsnorm(const moe_config* cfg, const void* x, const void* residual, const void* norm_w,
+                           void* res_out, void* xn, void* q, float* q_scale, void* stream);
+
+/* n_mats matrices [rows][cols] (bf16 or fp32, dtype a moe_dtype) to e4m3 in
+ * blocks of block_rows x 128, block_rows = 1 (activations) or 128 (weights).
+ *   q [n_mats][rows][cols],  scale [n_mats][ceil(rows/block_rows)][ceil(cols/128)]. */
+moe_status moe_quantize_fp8(int32_t dtype, int32_t block_rows, int32_t n_mats, int32_t rows, int32_t cols,
+                            const void* x, void* q, float* scale, void* stream);
+
+/* Bytes of workspace that moe_gemm_fp8 needs for these sizes; 0 if they are
+ * invalid.  Initialise it once with moe_workspace_init. */
+size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n_out, int32_t k);
+
+/* Block-scaled product, grouped by expert: for the rows r in
+ * [offsets[g], offsets[g+1]) of a,
+ *   c[r][n] = sum_kb a_scale[r][kb] * b_scale[g][n/128][kb] * sum_{k in block kb} a[r][k] * b[g][n][k].
+ * The sums inside a block of 128 and over the blocks are fp32; c is rounded
+ * once, to c_dtype (moe_dtype).
+ *   n_groups G in [1, 1024];  offsets [G+1] device, nondecreasing,
+ *   offsets[0] >= 0, offsets[G] <= max_rows; NULL = one group of max_rows rows
+ *   (a plain product).  Groups may be empty.
+ *   a [max_rows][k], a_scale [max_rows][ceil(k/128)], b [G][n_out][k],
+ *   b_scale [G][ceil(n_out/128)][ceil(k/128)], c [max_rows][n_out] out; rows
+ *   outside [offsets[0], offsets[G]) are not written.
+ * Any n_out; k % 16 == 0. */
+moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_rows, int32_t n_out, int32_t k,
+                        const void* a, const float* a_scale, const void* b, const float* b_scale, int32_t c_dtype,
+                        void* c, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace for moe_expert_ffn_fp8 and moe_layer_forward_fp8 with
+ * this config; 0 if it is invalid. */
+size_t moe_workspace_size_fp8(const moe_config* cfg);
+
+/* moe_expert_ffn on e4m3 operands: per group g,
+ *   t = silu(x . w_gate[g]) * (x . w_up[g]) in fp32, quantised per row and 128
+ *   hidden units as moe_quantize_fp8 does, and y = t . w_down[g],
+ * every product as in moe_gemm_fp8.  Groups, offsets and rows as there;
+ * x [max_rows][d] e4m3 with x_scale [max_rows][ceil(d/128)], y [max_rows][d] in
+ * the act dtype.  d % 16 == 0, d_ff % 16 == 0.  The e4m3 activation is kept
+ * in the workspace (moe_workspace_size_fp8 of a config with N*k >= max_rows). */
+moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int32_t* offsets, int32_t max_rows,
+                              const void* x, const float* x_scale, const void* w_gate, const float* w_gate_scale,
+                              const void* w_up, const float* w_up_scale, const void* w_down,
+                              const float* w_down_scale, int32_t d_ff, void* y, void* ws, size_t ws_bytes,
+                              void* stream);
+
+/* The whole forward pass with e4m3 experts, on one stream with no host
+ * synchronisation:
+ *   s = act(h + residual), xn = RMSNorm(s),
+ *   out = s + sum_{e in topk} gate_e * FFN_e(e4m3(xn)) [+ FFN_shared(e4m3(xn))].
+ * Router, routing, permutation, capacity and combine are those of
+ * moe_layer_forward (the router reads xn in the act dtype); the experts are
+ * moe_expert_ffn_fp8.
+ *   residual [N][d] or NULL (s = h); out [N][d] (may equal h or residual)
+ *   d, H and Hs multiples of 16; the rest as in moe_layer_forward. */
+moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* weights, const void* h,
+                                 const void* residual, const float* bias, void* out, const moe_routing* routing,
+                                 const moe_trace* trace, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, read and clear the workspace's device error word.
  * Returns MOE_OK, the recorded status (e.g. MOE_ERR_DEVICE_TIMEOUT) or
  * MOE_ERR_CUDA.  info (host, may be NULL) receives 4 int32 of detail

@@ -31,7 +31,8 @@ MOE_F32, MOE_BF16 = 0, 1
 ENTRY_POINTS = (
     "moe_status_string", "moe_version", "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_route_hash",
     "moe_permute", "moe_permute_noalloc", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_bias_update",
-    "moe_compute_load_stats", "moe_check_device_error", "moe_set_wait_timeout_ns", "moe_set_gemm_tiling",
+    "moe_compute_load_stats", "moe_add_rmsnorm", "moe_quantize_fp8", "moe_workspace_size_gemm_fp8", "moe_gemm_fp8",
+    "moe_workspace_size_fp8", "moe_expert_ffn_fp8", "moe_layer_forward_fp8", "moe_check_device_error", "moe_set_wait_timeout_ns", "moe_set_gemm_tiling",
     "moe_selftest_wait_timeout",
 )
 
@@ -51,6 +52,14 @@ class MoeConfig(ctypes.Structure):
 class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("norm_w", "w_router", "w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")]
+
+
+_FP8_MATRICES = ("w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")
+
+
+class MoeWeightsFp8(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("norm_w", "w_router", *(m + s for m in _FP8_MATRICES for s in ("", "_scale")))]
 
 
 class MoeRouting(ctypes.Structure):
@@ -85,6 +94,14 @@ def _load():
                                     ctypes.POINTER(MoeTrace), P, SZ, P]),
         "moe_bias_update": (I32, [I32, P, F, F, P, P]),
         "moe_compute_load_stats": (I32, [cfgp, P, P, P, P]),
+        "moe_add_rmsnorm": (I32, [cfgp, P, P, P, P, P, P, P, P]),
+        "moe_quantize_fp8": (I32, [I32, I32, I32, I32, I32, P, P, P, P]),
+        "moe_workspace_size_gemm_fp8": (SZ, [I32, I32, I32, I32]),
+        "moe_gemm_fp8": (I32, [I32, P, I32, I32, I32, P, P, P, P, I32, P, P, SZ, P]),
+        "moe_workspace_size_fp8": (SZ, [cfgp]),
+        "moe_expert_ffn_fp8": (I32, [cfgp, I32, P, I32, P, P, P, P, P, P, P, P, I32, P, P, SZ, P]),
+        "moe_layer_forward_fp8": (I32, [cfgp, ctypes.POINTER(MoeWeightsFp8), P, P, P, P, ctypes.POINTER(MoeRouting),
+                                        ctypes.POINTER(MoeTrace), P, SZ, P]),
         "moe_check_device_error": (I32, [P, SZ, P, P]),
         "moe_set_wait_timeout_ns": (I32, [I64]),
         "moe_set_gemm_tiling": (I32, [I32]),
@@ -164,15 +181,30 @@ def workspace_size(cfg: Config) -> int:
     return int(_lib.moe_workspace_size(ctypes.byref(cfg.c())))
 
 
-def workspace(cfg: Config, device="cuda", stream=None):
-    """Allocate (through torch) and initialise a workspace for ``cfg``."""
+def _new_workspace(n: int, where: str, device, stream):
     import torch
-    n = workspace_size(cfg)
     if n == 0:
-        raise MoEError(MOE_ERR_INVALID_ARG, "moe_workspace_size")
+        raise MoEError(MOE_ERR_INVALID_ARG, where)
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     _check(_lib.moe_workspace_init(ws.data_ptr(), n, _stream(stream)), "moe_workspace_init")
     return ws
+
+
+def workspace(cfg: Config, device="cuda", stream=None):
+    """Allocate (through torch) and initialise a workspace for ``cfg``."""
+    return _new_workspace(workspace_size(cfg), "moe_workspace_size", device, stream)
+
+
+def workspace_fp8(cfg: Config, device="cuda", stream=None):
+    """The workspace of moe_expert_ffn_fp8 and moe_layer_forward_fp8 for ``cfg``."""
+    n = int(_lib.moe_workspace_size_fp8(ctypes.byref(cfg.c())))
+    return _new_workspace(n, "moe_workspace_size_fp8", device, stream)
+
+
+def workspace_gemm_fp8(n_groups: int, max_rows: int, n_out: int, k: int, device="cuda", stream=None):
+    """The workspace of moe_gemm_fp8 for these sizes."""
+    n = int(_lib.moe_workspace_size_gemm_fp8(n_groups, max_rows, n_out, k))
+    return _new_workspace(n, "moe_workspace_size_gemm_fp8", device, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -222,25 +254,33 @@ def _weights_struct(w: dict) -> MoeWeights:
                         ("norm_w", "w_router", "w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")])
 
 
+def _routing_struct(routing: dict | None):
+    if routing is None:
+        return None
+    return MoeRouting(*[_ptr(routing.get(n)) for n in
+                        ("scores", "topk_idx", "topk_gate", "counts", "offsets", "slot_row", "row_token")])
+
+
+def _trace_struct(trace: dict | None, stream):
+    if trace is None:
+        return None
+    handles = []
+    for n in ("start", "routed", "permuted", "gate_up", "down", "shared", "combined"):
+        ev = trace.get(n)
+        if ev is not None and not ev.cuda_event:
+            ev.record(_torch_stream(stream))  # torch creates its events lazily, on the first record
+        handles.append(ev.cuda_event if ev is not None else None)
+    return MoeTrace(*handles)
+
+
 def moe_layer_forward(cfg: Config, weights: dict, h, bias, out, ws, routing: dict | None = None,
                       trace: dict | None = None, stream=None):
     """The whole layer on one stream.  ``routing``: optional dict of device
     output tensors (scores, topk_idx, topk_gate, counts, offsets, slot_row,
     row_token); ``trace``: optional dict of torch.cuda.Event per stage."""
     w = _weights_struct(weights)
-    r = None
-    if routing is not None:
-        r = MoeRouting(*[_ptr(routing.get(n)) for n in
-                         ("scores", "topk_idx", "topk_gate", "counts", "offsets", "slot_row", "row_token")])
-    tr = None
-    if trace is not None:
-        handles = []
-        for n in ("start", "routed", "permuted", "gate_up", "down", "shared", "combined"):
-            ev = trace.get(n)
-            if ev is not None and not ev.cuda_event:
-                ev.record(_torch_stream(stream))  # torch creates its events lazily, on the first record
-            handles.append(ev.cuda_event if ev is not None else None)
-        tr = MoeTrace(*handles)
+    r = _routing_struct(routing)
+    tr = _trace_struct(trace, stream)
     _check(_lib.moe_layer_forward(ctypes.byref(cfg.c()), ctypes.byref(w), _ptr(h), _ptr(bias), _ptr(out),
                                   ctypes.byref(r) if r is not None else None,
                                   ctypes.byref(tr) if tr is not None else None,
@@ -262,6 +302,52 @@ def moe_compute_load_stats(cfg: Config, counts, offsets, stats, stream=None):
     """stats: a device buffer of at least ctypes.sizeof(MoeLoadStats) bytes."""
     _check(_lib.moe_compute_load_stats(ctypes.byref(cfg.c()), _ptr(counts), _ptr(offsets), _ptr(stats),
                                        _stream(stream)), "moe_compute_load_stats")
+
+
+_DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16}
+
+
+def moe_add_rmsnorm(cfg: Config, x, residual, norm_w, res_out, xn, q, q_scale, stream=None):
+    """s = x + residual (residual may be None); res_out = s, xn = RMSNorm(s) * norm_w and (q, q_scale) = xn in e4m3
+    with a scale per 128 columns; each output may be None."""
+    _check(_lib.moe_add_rmsnorm(ctypes.byref(cfg.c()), _ptr(x), _ptr(residual), _ptr(norm_w), _ptr(res_out), _ptr(xn),
+                                _ptr(q), _ptr(q_scale), _stream(stream)), "moe_add_rmsnorm")
+
+
+def moe_quantize_fp8(dtype: str, block_rows: int, n_mats: int, rows: int, cols: int, x, q, scale, stream=None):
+    """n_mats matrices [rows][cols] ("bf16" or "f32") to e4m3 in blocks of block_rows (1 or 128) x 128."""
+    _check(_lib.moe_quantize_fp8(_DTYPES[dtype], block_rows, n_mats, rows, cols, _ptr(x), _ptr(q), _ptr(scale),
+                                 _stream(stream)), "moe_quantize_fp8")
+
+
+def moe_gemm_fp8(n_groups: int, offsets, max_rows: int, n_out: int, k: int, a, a_scale, b, b_scale, c_dtype: str, c,
+                 ws, stream=None):
+    """Rows [offsets[g], offsets[g+1]) of a times b[g]^T, e4m3 with block scales; offsets None: one group."""
+    _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, _ptr(a), _ptr(a_scale), _ptr(b),
+                             _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_gemm_fp8")
+
+
+def moe_expert_ffn_fp8(cfg: Config, n_groups: int, offsets, max_rows: int, x, x_scale, w_gate, w_gate_scale, w_up,
+                       w_up_scale, w_down, w_down_scale, d_ff: int, y, ws, stream=None):
+    """The grouped SwiGLU experts on e4m3 rows and weights with block scales."""
+    _check(_lib.moe_expert_ffn_fp8(ctypes.byref(cfg.c()), n_groups, _ptr(offsets), max_rows, _ptr(x), _ptr(x_scale),
+                                   _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up), _ptr(w_up_scale), _ptr(w_down),
+                                   _ptr(w_down_scale), d_ff, _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_expert_ffn_fp8")
+
+
+def moe_layer_forward_fp8(cfg: Config, weights: dict, h, residual, bias, out, ws, routing: dict | None = None,
+                          trace: dict | None = None, stream=None):
+    """The whole layer with e4m3 experts; ``weights``: norm_w, w_router and each
+    expert matrix with its ``<name>_scale``.  residual (or None) is added to h first."""
+    w = MoeWeightsFp8(*[_ptr(weights.get(n)) for n, _ in MoeWeightsFp8._fields_])
+    r = _routing_struct(routing)
+    tr = _trace_struct(trace, stream)
+    _check(_lib.moe_layer_forward_fp8(ctypes.byref(cfg.c()), ctypes.byref(w), _ptr(h), _ptr(residual), _ptr(bias),
+                                      _ptr(out), ctypes.byref(r) if r is not None else None,
+                                      ctypes.byref(tr) if tr is not None else None,
+                                      _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward_fp8")
 
 
 def moe_check_device_error(ws, stream=None):
