@@ -348,13 +348,14 @@ size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n
  *   n_groups G in [1, 1024];  offsets [G+1] device, nondecreasing,
  *   offsets[0] >= 0, offsets[G] <= max_rows; NULL = one group of max_rows rows
  *   (a plain product).  Groups may be empty.
- *   a [max_rows][k], a_scale [max_rows][ceil(k/128)], b [G][n_out][k],
+ *   a [max_rows][k], its rows lda >= k bytes apart (lda % 16 == 0),
+ *   a_scale [max_rows][ceil(k/128)], b [G][n_out][k],
  *   b_scale [G][ceil(n_out/128)][ceil(k/128)], c [max_rows][n_out] out; rows
  *   outside [offsets[0], offsets[G]) are not written.
  * Any n_out; k % 16 == 0. */
 moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_rows, int32_t n_out, int32_t k,
-                        const void* a, const float* a_scale, const void* b, const float* b_scale, int32_t c_dtype,
-                        void* c, void* ws, size_t ws_bytes, void* stream);
+                        const void* a, int64_t lda, const float* a_scale, const void* b, const float* b_scale,
+                        int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace for moe_expert_ffn_fp8 and moe_layer_forward_fp8 with
  * this config; 0 if it is invalid. */
@@ -364,14 +365,14 @@ size_t moe_workspace_size_fp8(const moe_config* cfg);
  *   t = silu(x . w_gate[g]) * (x . w_up[g]) in fp32, quantised per row and 128
  *   hidden units as moe_quantize_fp8 does, and y = t . w_down[g],
  * every product as in moe_gemm_fp8.  Groups, offsets and rows as there;
- * x [max_rows][d] e4m3 with x_scale [max_rows][ceil(d/128)], y [max_rows][d] in
- * the act dtype.  d % 16 == 0, d_ff % 16 == 0.  The e4m3 activation is kept
+ * x [max_rows][d] e4m3, its rows ldx >= d bytes apart (ldx % 16 == 0), with
+ * x_scale [max_rows][ceil(d/128)], y [max_rows][d] in the act dtype.  d % 16 == 0, d_ff % 16 == 0.  The e4m3 activation is kept
  * in the workspace (moe_workspace_size_fp8 of a config with N*k >= max_rows). */
 moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int32_t* offsets, int32_t max_rows,
-                              const void* x, const float* x_scale, const void* w_gate, const float* w_gate_scale,
-                              const void* w_up, const float* w_up_scale, const void* w_down,
-                              const float* w_down_scale, int32_t d_ff, void* y, void* ws, size_t ws_bytes,
-                              void* stream);
+                              const void* x, int64_t ldx, const float* x_scale, const void* w_gate,
+                              const float* w_gate_scale, const void* w_up, const float* w_up_scale,
+                              const void* w_down, const float* w_down_scale, int32_t d_ff, void* y, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /* The whole forward pass with e4m3 experts, on one stream with no host
  * synchronisation:

@@ -97,9 +97,9 @@ def _load():
         "moe_add_rmsnorm": (I32, [cfgp, P, P, P, P, P, P, P, P]),
         "moe_quantize_fp8": (I32, [I32, I32, I32, I32, I32, P, P, P, P]),
         "moe_workspace_size_gemm_fp8": (SZ, [I32, I32, I32, I32]),
-        "moe_gemm_fp8": (I32, [I32, P, I32, I32, I32, P, P, P, P, I32, P, P, SZ, P]),
+        "moe_gemm_fp8": (I32, [I32, P, I32, I32, I32, P, I64, P, P, P, I32, P, P, SZ, P]),
         "moe_workspace_size_fp8": (SZ, [cfgp]),
-        "moe_expert_ffn_fp8": (I32, [cfgp, I32, P, I32, P, P, P, P, P, P, P, P, I32, P, P, SZ, P]),
+        "moe_expert_ffn_fp8": (I32, [cfgp, I32, P, I32, P, I64, P, P, P, P, P, P, P, I32, P, P, SZ, P]),
         "moe_layer_forward_fp8": (I32, [cfgp, ctypes.POINTER(MoeWeightsFp8), P, P, P, P, ctypes.POINTER(MoeRouting),
                                         ctypes.POINTER(MoeTrace), P, SZ, P]),
         "moe_check_device_error": (I32, [P, SZ, P, P]),
@@ -320,18 +320,32 @@ def moe_quantize_fp8(dtype: str, block_rows: int, n_mats: int, rows: int, cols: 
                                  _stream(stream)), "moe_quantize_fp8")
 
 
+def _rows(t, cols: int):
+    """(pointer, bytes between rows) of a matrix of one-byte elements whose rows may lie apart."""
+    if t is None or isinstance(t, int):
+        return t, cols
+    if t.dim() != 2 or t.is_contiguous():
+        return _ptr(t), cols
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("the rows of a matrix passed to the MoE library must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
 def moe_gemm_fp8(n_groups: int, offsets, max_rows: int, n_out: int, k: int, a, a_scale, b, b_scale, c_dtype: str, c,
                  ws, stream=None):
-    """Rows [offsets[g], offsets[g+1]) of a times b[g]^T, e4m3 with block scales; offsets None: one group."""
-    _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, _ptr(a), _ptr(a_scale), _ptr(b),
+    """Rows [offsets[g], offsets[g+1]) of a times b[g]^T, e4m3 with block scales; offsets None: one group.
+    The rows of a may lie apart (a slice of a wider buffer)."""
+    a_ptr, lda = _rows(a, k)
+    _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, a_ptr, lda, _ptr(a_scale), _ptr(b),
                              _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_gemm_fp8")
 
 
 def moe_expert_ffn_fp8(cfg: Config, n_groups: int, offsets, max_rows: int, x, x_scale, w_gate, w_gate_scale, w_up,
                        w_up_scale, w_down, w_down_scale, d_ff: int, y, ws, stream=None):
-    """The grouped SwiGLU experts on e4m3 rows and weights with block scales."""
-    _check(_lib.moe_expert_ffn_fp8(ctypes.byref(cfg.c()), n_groups, _ptr(offsets), max_rows, _ptr(x), _ptr(x_scale),
+    """The grouped SwiGLU experts on e4m3 rows and weights with block scales; the rows of x may lie apart."""
+    x_ptr, ldx = _rows(x, cfg.d_model)
+    _check(_lib.moe_expert_ffn_fp8(ctypes.byref(cfg.c()), n_groups, _ptr(offsets), max_rows, x_ptr, ldx, _ptr(x_scale),
                                    _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up), _ptr(w_up_scale), _ptr(w_down),
                                    _ptr(w_down_scale), d_ff, _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_expert_ffn_fp8")

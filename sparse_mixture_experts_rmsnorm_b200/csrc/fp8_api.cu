@@ -99,6 +99,7 @@ static moe_status ffn_fp8_impl(const moe_config* c, Fp8Gemm p, Fp8Operand w_down
   Fp8Operand act;
   act.q = (uint8_t*)wsp(ws, L.act);
   act.scale = (float*)wsp(ws, L.act_s);
+  act.ld = d_ff;
   p.hdr = (int32_t*)wsp(ws, L.hdr);
   p.epi = EPI_SWIGLU;
   p.nout = d_ff;
@@ -121,8 +122,9 @@ static moe_status ffn_fp8_impl(const moe_config* c, Fp8Gemm p, Fp8Operand w_down
   return launch_gemm_fp8(p, s);
 }
 
-static Fp8Operand operand(const void* q, const float* scale) {
+static Fp8Operand operand(const void* q, const float* scale, int64_t ld = 0) {
   Fp8Operand o;
+  o.ld = ld;
   o.q = (const uint8_t*)q;
   o.scale = scale;
   return o;
@@ -160,19 +162,20 @@ size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n
 }
 
 moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_rows, int32_t n_out, int32_t k,
-                        const void* a, const float* a_scale, const void* b, const float* b_scale, int32_t c_dtype,
-                        void* c, void* ws, size_t ws_bytes, void* stream) {
+                        const void* a, int64_t lda, const float* a_scale, const void* b, const float* b_scale,
+                        int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream) {
   NvtxScope range("moe_gemm_fp8");
   const size_t need = moe_workspace_size_gemm_fp8(n_groups, max_rows, n_out, k);
   if (need == 0 || (offsets == nullptr && n_groups != 1)) return MOE_ERR_INVALID_ARG;
   if (c_dtype != MOE_F32 && c_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || ((uintptr_t)ws % 256) != 0) return MOE_ERR_INVALID_ARG;
   if (max_rows > 0 && (!a || !a_scale || !b || !b_scale || !c)) return MOE_ERR_INVALID_ARG;
-  if (k % 16 || misaligned({a, b}) || (int64_t)n_groups * n_out > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (lda < k) return MOE_ERR_INVALID_ARG;
+  if (k % 16 || lda % 16 || misaligned({a, b}) || (int64_t)n_groups * n_out > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   Fp8Gemm g;
   g.epi = c_dtype == MOE_BF16 ? EPI_STORE : EPI_F32;
-  g.a = operand(a, a_scale);
+  g.a = operand(a, a_scale, lda);
   g.b = operand(b, b_scale);
   g.offsets = offsets;
   g.groups = n_groups;
@@ -190,10 +193,10 @@ size_t moe_workspace_size_fp8(const moe_config* cfg) {
 }
 
 moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int32_t* offsets, int32_t max_rows,
-                              const void* x, const float* x_scale, const void* w_gate, const float* w_gate_scale,
-                              const void* w_up, const float* w_up_scale, const void* w_down,
-                              const float* w_down_scale, int32_t d_ff, void* y, void* ws, size_t ws_bytes,
-                              void* stream) {
+                              const void* x, int64_t ldx, const float* x_scale, const void* w_gate,
+                              const float* w_gate_scale, const void* w_up, const float* w_up_scale,
+                              const void* w_down, const float* w_down_scale, int32_t d_ff, void* y, void* ws,
+                              size_t ws_bytes, void* stream) {
   NvtxScope range("moe_expert_ffn_fp8");
   MOE_TRY(check_fp8(cfg, ws, ws_bytes));
   if (n_groups < 1 || n_groups > moe::TC_MAX_GROUPS || max_rows < 0 || d_ff < 1) return MOE_ERR_INVALID_ARG;
@@ -206,9 +209,10 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
   if (max_rows == 0) return MOE_OK;
   if (!x || !x_scale || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !w_down || !w_down_scale || !y)
     return MOE_ERR_INVALID_ARG;
-  if (misaligned({x, w_gate, w_up, w_down})) return MOE_ERR_UNSUPPORTED;
+  if (ldx < cfg->d_model) return MOE_ERR_INVALID_ARG;
+  if (ldx % 16 || misaligned({x, w_gate, w_up, w_down})) return MOE_ERR_UNSUPPORTED;
   Fp8Gemm p;
-  p.a = operand(x, x_scale);
+  p.a = operand(x, x_scale, ldx);
   p.b = operand(w_gate, w_gate_scale);
   p.b2 = operand(w_up, w_up_scale);
   p.offsets = offsets;
@@ -289,7 +293,7 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
   MOE_TRY(mark(trace ? trace->permuted : nullptr, "gate_up"));
   const int R = (int)L.rows;
   Fp8Gemm p;
-  p.a = operand(xq_perm, xs_perm);
+  p.a = operand(xq_perm, xs_perm, d);
   p.b = operand(w->w_gate, w->w_gate_scale);
   p.b2 = operand(w->w_up, w->w_up_scale);
   p.offsets = L.fold ? offs_ext : offsets;
@@ -299,7 +303,7 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
   if (L.fold) {
     p.sb = operand(w->ws_gate, w->ws_gate_scale);
     p.sb2 = operand(w->ws_up, w->ws_up_scale);
-    p.sa = operand(xq, xs);
+    p.sa = operand(xq, xs, d);
     p.sa_rows = N;
     down_shared = operand(w->ws_down, w->ws_down_scale);
   }
@@ -311,7 +315,7 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
   MOE_TRY(mark(trace ? trace->down : nullptr, "shared"));
   if (y_shared && N > 0) {
     Fp8Gemm ps;
-    ps.a = operand(xq, xs);
+    ps.a = operand(xq, xs, d);
     ps.b = operand(w->ws_gate, w->ws_gate_scale);
     ps.b2 = operand(w->ws_up, w->ws_up_scale);
     ps.max_rows = N;

@@ -50,10 +50,12 @@ __global__ void __launch_bounds__(256) gemm_fp8_simple_kernel(const Fp8Args args
   const bool sh = a.sb.q != nullptr && g == a.groups - 1;
   const uint8_t* A = a.a.q;
   const float* As = a.a.scale;
+  int64_t ld = a.a.ld;
   int shift = 0;
   if (sh && a.sa.q != nullptr) {
     A = a.sa.q;
     As = a.sa.scale;
+    ld = a.sa.ld;
     shift = a.offsets[g];
   }
   const int warp = warp_id(), lane = lane_id();
@@ -64,7 +66,7 @@ __global__ void __launch_bounds__(256) gemm_fp8_simple_kernel(const Fp8Args args
       __syncthreads();
       for (int i = threadIdx.x; i < 32 * 32; i += 256) {
         const int r = i / 32, k = k0 + i % 32;
-        xs[r][i % 32] = (row0 + r < row_end && k < a.k) ? e4m3_value(A[(size_t)(row0 + r - shift) * a.k + k]) : 0.f;
+        xs[r][i % 32] = (row0 + r < row_end && k < a.k) ? e4m3_value(A[(size_t)(row0 + r - shift) * ld + k]) : 0.f;
       }
       for (int b = 0; b < NB; ++b) {
         const uint8_t* W = sh ? (b ? a.sb2.q : a.sb.q) : (b ? a.b2.q : a.b.q) + (size_t)g * a.nout * a.k;

@@ -17,6 +17,7 @@ moe_status launch_quantize(int dtype, int block_rows, int mats, int rows, int co
 struct Fp8Operand {
   const uint8_t* q = nullptr;
   const float* scale = nullptr;
+  int64_t ld = 0;  // bytes between rows (the row operands a, sa)
 };
 
 // Arguments of a grouped block-scaled e4m3 product.

@@ -61,8 +61,8 @@ def test_quantize_refusals():
 
 
 def test_gemm_refusals():
-    def gemm(g=1, offs=None, rows=64, n=256, k=256, a=256, sa=256, b=256, sb=256, t=1, c=256, ws=256, bytes=BIG):
-        return lib.moe_gemm_fp8(g, offs, rows, n, k, a, sa, b, sb, t, c, ws, bytes, None)
+    def gemm(g=1, offs=None, rows=64, n=256, k=256, a=256, sa=256, b=256, sb=256, t=1, c=256, ws=256, bytes=BIG, lda=None):
+        return lib.moe_gemm_fp8(g, offs, rows, n, k, a, k if lda is None else lda, sa, b, sb, t, c, ws, bytes, None)
 
     assert gemm(g=2) == BAD and gemm(g=0, offs=256) == BAD and gemm(g=1025, offs=256) == BAD
     assert gemm(rows=-1) == BAD and gemm(n=0) == BAD and gemm(k=0) == BAD and gemm(t=2) == BAD
@@ -70,6 +70,7 @@ def test_gemm_refusals():
         assert gemm(**{p: None}) == BAD, p
     assert gemm(ws=128) == BAD
     assert gemm(k=264) == UNSUPPORTED and gemm(a=264) == UNSUPPORTED and gemm(b=257) == UNSUPPORTED
+    assert gemm(lda=240) == BAD and gemm(lda=264) == UNSUPPORTED
     assert gemm(g=1024, offs=256, n=1 << 22) == UNSUPPORTED
     assert gemm(bytes=128) == WORKSPACE
     assert gemm(rows=0, a=None, sa=None, b=None, sb=None, c=None) == moe.MOE_OK
@@ -78,10 +79,10 @@ def test_gemm_refusals():
 def test_ffn_refusals():
     PTRS = ("x", "x_scale", "w_gate", "w_gate_scale", "w_up", "w_up_scale", "w_down", "w_down_scale", "y")
 
-    def ffn(cfg=None, g=1, offs=None, rows=64, h=128, ws=256, bytes=BIG, **null):
+    def ffn(cfg=None, ldx=256, g=1, offs=None, rows=64, h=128, ws=256, bytes=BIG, **null):
         p = {n: 256 for n in PTRS}
         p.update(null)
-        return lib.moe_expert_ffn_fp8(ctypes.byref((cfg or _cfg()).c()), g, offs, rows, *(p[n] for n in PTRS[:-1]), h,
+        return lib.moe_expert_ffn_fp8(ctypes.byref((cfg or _cfg()).c()), g, offs, rows, p["x"], ldx, *(p[n] for n in PTRS[1:-1]), h,
                                       p["y"], ws, bytes, None)
 
     assert ffn(cfg=_cfg(top_k=9)) == BAD and ffn(ws=None) == BAD and ffn(ws=128) == BAD
@@ -90,6 +91,7 @@ def test_ffn_refusals():
         assert ffn(**{n: None}) == BAD, n
     assert ffn(cfg=_cfg(d_model=264)) == UNSUPPORTED and ffn(cfg=_cfg(d_ff=136)) == UNSUPPORTED
     assert ffn(h=24) == UNSUPPORTED and ffn(w_up=264) == UNSUPPORTED
+    assert ffn(ldx=240) == BAD and ffn(ldx=264) == UNSUPPORTED
     assert ffn(bytes=256) == WORKSPACE
     assert ffn(rows=100000) == WORKSPACE
     assert ffn(h=16, rows=1024) == WORKSPACE  # the codes fit, their scales do not
@@ -120,5 +122,7 @@ def test_python_wrapper_refuses_strided_tensors():
     x = torch.zeros(4, 64)[:, ::2]
     with pytest.raises(ValueError):
         moe.moe_quantize_fp8("f32", 1, 1, 4, 32, x, None, None, stream=0)
+    with pytest.raises(ValueError):  # columns apart; rows may be
+        moe.moe_gemm_fp8(1, None, 4, 32, 32, x, None, None, None, "f32", None, torch.zeros(256), stream=0)
     with pytest.raises(KeyError):
         moe.moe_quantize_fp8("f16", 1, 1, 4, 32, None, None, None, stream=0)

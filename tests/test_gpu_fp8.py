@@ -216,6 +216,28 @@ def test_grouped_gemm(env, out, name, n, k):
     assert moe.moe_check_device_error(ws)[0] == 0
 
 
+def test_rows_that_lie_apart(env):
+    """a (and the FFN's x) may be a slice of a wider buffer: the same bits as from a packed copy."""
+    torch, moe = env
+    rows, n, k = 200, 256, 400
+    aq, as_, bq, bs = _operands(torch, [rows], n, k)
+    wide = torch.full((rows, 512), 0x7F, dtype=torch.uint8, device="cuda").view(f8.E4M3)  # NaN around the slice
+    wide[:, 16:16 + k] = aq
+    ws = moe.workspace_gemm_fp8(1, rows, n, k)
+    c = torch.empty(2, rows, n, device="cuda")
+    moe.moe_gemm_fp8(1, None, rows, n, k, aq, as_, bq, bs, "f32", c[0], ws)
+    moe.moe_gemm_fp8(1, None, rows, n, k, wide[:, 16:16 + k], as_, bq, bs, "f32", c[1], ws)
+    assert torch.equal(c[0], c[1])
+    _, _, uq, us = _operands(torch, [1], n, k)
+    _, _, dq, ds = _operands(torch, [1], k, n)
+    cfg = moe.Config(rows, k, 1, 1, n)
+    ws = moe.workspace_fp8(cfg)
+    y = torch.empty(2, rows, k, dtype=torch.bfloat16, device="cuda")
+    for x, out in ((aq, y[0]), (wide[:, 16:16 + k], y[1])):
+        moe.moe_expert_ffn_fp8(cfg, 1, None, rows, x, as_, bq, bs, uq, us, dq, ds, n, out, ws)
+    assert torch.equal(y[0], y[1])
+
+
 def test_rows_before_the_first_group_stay(env):
     torch, moe = env
     sizes, n, k = [11, 40], 64, 256
