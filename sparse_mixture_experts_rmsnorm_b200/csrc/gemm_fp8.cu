@@ -1,137 +1,1016 @@
-// Grouped product of e4m3 operands with block scales:
+// Grouped product of e4m3 operands with block scales on SM pairs
+// (tcgen05.mma.cta_group::2.kind::f8f6f4):
 //   C[r][n] = sum_kb sa[r][kb] * sb[g][n / 128][kb] * sum_{k in kb} A[r][k] * B[g][n][k]
-// for the rows r of group g, kb running over blocks of 128 columns.  The inner
-// sums and the sum over blocks are fp32.
+// for the rows r of group (expert) g, kb running over blocks of 128 columns.
+// Epilogues: bf16 or fp32 results, or for the experts' gate and up projections
+//   t = silu(gate) * up  in fp32, quantised per row and 128 hidden units.
+//
+// The operands are swapped as in gemm_swap.cu: 256 weight rows per SM pair on
+// the MMA's M side, a chunk of up to 256 of the group's rows on its N side (a
+// group of m rows is cut into ceil(m / 256) equal chunks, padded to 16 rows).
+//
+// Scales.  They change every 128 columns, so every k-block of 128 gets its own
+// accumulator in one of two 256-column TMEM slots, and eight epilogue warps per
+// CTA add it, times its scales, to fp32 sums in registers: 128 of them per
+// thread, acc += v * (sa * sb) as packed pairs.  A warp reads TMEM in the
+// 16x256b shape (lane l holds rows l / 4 and l / 4 + 8, columns 2 (l % 4) and
+// + 1 of every eight), so one product sa * sb, read from shared memory, serves
+// four values.  Two warps beside the producer and the MMA issuer form those
+// products a few k-blocks ahead.
+//
+// Gate and up.  One 5-D view over both matrices (their distance is a stride)
+// interleaves them in shared memory, eight gate rows, eight up rows, so a
+// thread holds both values of a hidden unit and the activation needs no
+// exchange.  A pair's tile is 128 hidden units, one block of the result's
+// scales: only each row's largest magnitude crosses between the CTAs.
+//
+// Roles (384 threads per CTA, clusters of two; the register file is split
+// between the roles with setmaxnreg):
+//   warp 0      TMA producer in both CTAs; 3-stage ring of 64 KiB, two k-blocks
+//               per stage and (K % 128 == 0) one load per operand and stage;
+//   warp 1      TMEM allocation; in the even CTA lane 0 issues the MMAs;
+//   warps 2, 3  scale products, alternating k-blocks, into a ring of 4 slots;
+//   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
+//               of the chunk's columns.
+// Tiles run group by group, a group's chunks in runs of eight per weight tile,
+// and are claimed from a counter in the workspace header that the last pair to
+// finish sets back to zero.  Data that crosses to the other CTA travels by
+// st.async; no TMA load uses cluster multicast.  Every wait is bounded: on
+// time-out the block records MOE_ERR_DEVICE_TIMEOUT, stops issuing work, drains
+// and returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "gemm_fp8_kernels.h"
 #include "quant_common.cuh"
+#include "tcgen05_pair.cuh"
 
 namespace moe {
 
-struct Fp8Args {
-  moe_host::Fp8Gemm g;
-};
+constexpr int F_BK = 128;                             // k-block: 128 e4m3 codes, one 128-byte swizzle row
+constexpr int F_KB = 2;                               // k-blocks per stage
+constexpr int F_STAGES = 3;
+constexpr int F_KBLK_BYTES = 128 * F_BK;              // one k-block of 128 rows: 16 KiB
+constexpr int F_A_BYTES = F_KB * F_KBLK_BYTES;        // this CTA's 128 weight rows
+constexpr int F_STAGE_BYTES = 2 * F_A_BYTES;          // and up to 128 rows of the chunk
+constexpr int F_THREADS = 384;
+constexpr int F_EPI_WARP0 = 4, F_EPI_WARPS = 8;
+constexpr int F_CHUNK = 256;                          // most rows of a group in one tile
+constexpr int F_RUN = 8;                              // chunks that walk a group's weight tiles together
+constexpr int F_XMAPS = 16;                           // row boxes of 8, 16, ..., 128 rows
+constexpr int F_TRING = 8;
+constexpr int F_SLOTS = 4;                            // k-blocks of scale products ahead
+// readers of a published tile index: even CTA: MMA thread, 2 scale and 8 epilogue
+// warps; odd CTA: producer, 2 and 8
+constexpr int F_TRING_READERS = 22;
+constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's 16 x 32 bf16 output block
+constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;
+constexpr int F_CLAIM_WORD = 40, F_DONE_WORD = 41;    // header words: tiles claimed, pairs finished
 
-__device__ __forceinline__ float silu_f(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-
-__device__ __forceinline__ float e4m3_value(uint8_t v) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+template <int EPI>
+constexpr int f8_mats() {  // weight matrices per tile
+  return EPI == moe_host::EPI_SWIGLU ? 2 : 1;
+}
+template <int EPI>
+constexpr int f8_smem_bytes() {
+  return F_STAGES * F_STAGE_BYTES + F_SLOTS * f8_mats<EPI>() * F_CHUNK * 4 +
+         (EPI == moe_host::EPI_STORE ? F_EPI_WARPS * F_OUT_BYTES : 0) + 1024;  // + alignment slack
 }
 
-// 32 rows x 128 columns per block of 256 threads: warp w takes rows 4w .. 4w + 3,
-// lane l columns l, l + 32, l + 64, l + 96.
-template <int EPI>
-__global__ void __launch_bounds__(256) gemm_fp8_simple_kernel(const Fp8Args args) {
-  const moe_host::Fp8Gemm& a = args.g;
-  constexpr int NB = EPI == moe_host::EPI_SWIGLU ? 2 : 1;
-  __shared__ float xs[32][33];
-  __shared__ float ws[NB][128][33];
-  __shared__ int tile_sh[3];
-  if (threadIdx.x == 0) {
-    int t = blockIdx.y, g = 0;
-    const int groups = a.offsets ? a.groups : 1;
-    tile_sh[0] = -1;
-    for (; g < groups; ++g) {
-      const int b = a.offsets ? a.offsets[g] : 0, e = a.offsets ? a.offsets[g + 1] : a.max_rows;
-      const int tiles = (e - b + 31) / 32;
-      if (t < tiles) {
-        tile_sh[0] = g;
-        tile_sh[1] = b + t * 32;
-        tile_sh[2] = e;
-        break;
+struct Fp8Maps {
+  CUtensorMap w, ws;       // routed and shared weights
+  CUtensorMap x[F_XMAPS];  // the rows: x[i] has boxes of 8 (i + 1) rows
+  CUtensorMap xs[F_XMAPS]; // the shared group's rows when they come from their own tensor
+};
+
+struct Fp8Args {
+  const int32_t* offsets;  // [G+1] device, or nullptr: one group of max_rows rows
+  int groups, max_rows;
+  int nout;                // output columns per group
+  int nk;                  // k-blocks
+  int n_o;                 // weight tiles per group
+  int view;                // 1: the maps bring two k-blocks per load (K % 128 == 0)
+  int nnb;                 // scale blocks along n
+  const float *as, *sas;               // row scales, and those of the shared group's own rows
+  const float *bs[2], *sbs[2];         // weight scales, in the order of the matrices in a tile
+  int up_first, s_up_first;            // SwiGLU: the up matrix comes first in a tile (it lies lower in memory)
+  void* c;
+  float* c_scale;
+  int vec;                 // 1: 16-byte stores of whole groups of 8 columns
+  int shared_group, shared_a;
+  int32_t* hdr;
+  uint64_t wait_ns;
+};
+
+enum { F_SITE_RING = 8, F_SITE_SCALE = 9, F_SITE_AMAX = 10 };
+
+// ---- tiles --------------------------------------------------------------------
+struct Fp8Tile {
+  int group, row0, rows, n, o;  // rows [row0, row0 + rows) of C; n = rows rounded up to 16; weight tile o
+};
+
+__device__ __forceinline__ int f8_chunks(int m) { return (m + F_CHUNK - 1) / F_CHUNK; }
+
+// One warp: prefix[g] = first tile of group g (n_o tiles per chunk).
+__device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int groups, int n_o) {
+  const int lane = lane_id();
+  int carry = 0;
+  for (int base = 0; base < groups; base += 32) {
+    const int g = base + lane;
+    const int v = g < groups ? f8_chunks(offs[g + 1] - offs[g]) * n_o : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (g < groups) prefix[g] = carry + x - v;
+    carry += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) prefix[groups] = carry;
+}
+
+__device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, int groups, int n_o) {
+  int lo = 0, hi = groups - 1;  // last g with prefix[g] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const int m = offs[lo + 1] - offs[lo];
+  const int ch = f8_chunks(m);
+  const int nc = ((m + ch - 1) / ch + 15) & ~15;
+  const int local = t - prefix[lo];
+  const int run = local / (n_o * F_RUN);
+  const int rem = local - run * n_o * F_RUN;
+  const int in_run = min(F_RUN, ch - run * F_RUN);
+  const int c = run * F_RUN + rem % in_run;
+  Fp8Tile tl;
+  tl.group = lo;
+  tl.o = rem / in_run;
+  tl.row0 = offs[lo] + c * nc;
+  tl.rows = max(0, min(nc, m - c * nc));
+  tl.n = max(16, (tl.rows + 15) & ~15);
+  return tl;
+}
+
+// ---- waits --------------------------------------------------------------------
+__device__ __forceinline__ bool f8_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One thread's bounded wait; CLUSTER: a barrier that the other CTA arrives on.
+template <bool CLUSTER>
+__device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, const Fp8Args& a, volatile int* abort,
+                                        int site) {
+  auto poll = [&] { return CLUSTER ? f8_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (poll()) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t polls = 1;; ++polls) {
+    if (poll()) return true;
+    if ((polls & 63u) == 0u) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 >= a.wait_ns) {
+        record_error(a.hdr, MOE_ERR_DEVICE_TIMEOUT, KID_GEMM_FP8, blockIdx.x, site);
+        *abort = 1;
+        return false;
       }
-      t -= tiles;
     }
   }
-  __syncthreads();
-  const int g = tile_sh[0], row0 = tile_sh[1], row_end = tile_sh[2];
-  if (g < 0) return;
-  const int n0 = blockIdx.x * 128;
-  const int nkb = (a.k + 127) / 128, nnb = (a.nout + 127) / 128;
-  const bool sh = a.sb.q != nullptr && g == a.groups - 1;
-  const uint8_t* A = a.a.q;
-  const float* As = a.a.scale;
-  int64_t ld = a.a.ld;
-  int shift = 0;
-  if (sh && a.sa.q != nullptr) {
-    A = a.sa.q;
-    As = a.sa.scale;
-    ld = a.sa.ld;
-    shift = a.offsets[g];
-  }
+}
+
+// Every lane waits; true when all of them saw the phase complete.
+template <bool CLUSTER>
+__device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, const Fp8Args& a, volatile int* abort,
+                                             int site) {
+  const bool ok = f8_wait<CLUSTER>(bar, parity, a, abort, site);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// ---- TMA, MMA and TMEM ----------------------------------------------------------
+__device__ __forceinline__ void f8_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  tma_load_2d_pair(dst, map, bar, c0, c1);
+}
+__device__ __forceinline__ void f8_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void f8_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(0), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void f8_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%3, %3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(0), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 operands, fp32 accumulation, K = 32.
+__device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B
+// e4m3 (bits 7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
+constexpr uint32_t f8_idesc(int m, int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// 16 TMEM lanes x 32 columns: register 4 j + i of lane l holds row l / 4 + 8 (i / 2),
+// column 8 j + 2 (l % 4) + i % 2.
+#define MOE_TMEM_LD16x32(taddr, r)                                                                                  \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "   \
+               "%13, %14, %15}, [%16];"                                                                             \
+               : "=r"((r)[0]), "=r"((r)[1]), "=r"((r)[2]), "=r"((r)[3]), "=r"((r)[4]), "=r"((r)[5]), "=r"((r)[6]), \
+                 "=r"((r)[7]), "=r"((r)[8]), "=r"((r)[9]), "=r"((r)[10]), "=r"((r)[11]), "=r"((r)[12]),             \
+                 "=r"((r)[13]), "=r"((r)[14]), "=r"((r)[15])                                                        \
+               : "r"(taddr))
+
+// Waits for this thread's TMEM loads; the registers pass through it, so no use of them can move above it.
+#define MOE_TMEM_WAIT16(r)                                                                                          \
+  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                                     \
+               : "+r"((r)[0]), "+r"((r)[1]), "+r"((r)[2]), "+r"((r)[3]), "+r"((r)[4]), "+r"((r)[5]), "+r"((r)[6]), \
+                 "+r"((r)[7]), "+r"((r)[8]), "+r"((r)[9]), "+r"((r)[10]), "+r"((r)[11]), "+r"((r)[12]),             \
+                 "+r"((r)[13]), "+r"((r)[14]), "+r"((r)[15])                                                        \
+               :                                                                                                    \
+               : "memory")
+
+__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpack64(uint64_t v) {
+  uint32_t lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
+  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+}
+// two fp32 FMAs, each rounded once
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t v, uint64_t s) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
+}
+
+// Place of column c (0 .. 127) of a half in a row of scale products: the four
+// values that a lane takes for two groups of eight columns lie together.
+__device__ __forceinline__ int f8_scale_at(int c) {
+  return (c & ~15) + ((c & 6) << 1) + ((c & 8) >> 2) + (c & 1);
+}
+
+// silu(z) = z / (1 + e^-z), the fast exp and divide intrinsics: about 1e-6
+// relative error, far below the e4m3 rounding that follows.
+__device__ __forceinline__ float f8_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+
+// Byte transpose over the four lanes l, l ^ 4, l ^ 8, l ^ 12: lane i = (l / 4) % 4
+// of them gets byte i of every lane's word, in lane order.
+__device__ __forceinline__ uint32_t f8_transpose_bytes(uint32_t w) {
+  const bool b0 = lane_id() & 4, b1 = lane_id() & 8;
+  // trade 16-bit halves with the lane two apart, then bytes with the neighbour
+  uint32_t p = __shfl_xor_sync(0xffffffffu, w, 8);
+  w = b1 ? __byte_perm(w, p, 0x3276) : __byte_perm(w, p, 0x5410);
+  p = __shfl_xor_sync(0xffffffffu, w, 4);
+  return b0 ? __byte_perm(w, p, 0x3715) : __byte_perm(w, p, 0x6240);
+}
+
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
+    gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args args) {
+  constexpr bool SWIGLU = EPI == moe_host::EPI_SWIGLU;
+  constexpr int MATS = f8_mats<EPI>();
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[F_STAGES];   // used in the even CTA
+  __shared__ __align__(8) uint64_t empty_bar[F_STAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA
+  __shared__ __align__(8) uint64_t sfull_bar[F_SLOTS];   // scale products of a k-block
+  __shared__ __align__(8) uint64_t sempty_bar[F_SLOTS];
+  __shared__ __align__(8) uint64_t amax_bar;             // SwiGLU: every warp's magnitudes are in amax_sh
+  __shared__ __align__(8) uint64_t peer_bar[2];          //         the other CTA's have arrived
+  __shared__ __align__(8) uint64_t inv_bar;              //         1 / scale of every row is in inv_sh
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t tr_full[F_TRING];     // a tile index is in tile_ring[j] (both CTAs)
+  __shared__ __align__(8) uint64_t tr_empty[F_TRING];    // every reader has taken it (even CTA)
+  __shared__ volatile int tile_ring[F_TRING];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ volatile int abort_flag;
+  __shared__ int offs_sh[TC_MAX_GROUPS + 1];
+  __shared__ int prefix_sh[TC_MAX_GROUPS + 1];
+  __shared__ unsigned amax_sh[SWIGLU ? F_CHUNK : 1];
+  __shared__ volatile float peer_sh[SWIGLU ? 2 : 1][SWIGLU ? F_CHUNK : 1];
+  __shared__ __align__(16) float inv_sh[SWIGLU ? F_CHUNK : 4];
+
   const int warp = warp_id(), lane = lane_id();
-  float acc[NB][4][4] = {};
-  for (int kb = 0; kb < nkb; ++kb) {
-    float in[NB][4][4] = {};
-    for (int k0 = kb * 128; k0 < kb * 128 + 128; k0 += 32) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < 32 * 32; i += 256) {
-        const int r = i / 32, k = k0 + i % 32;
-        xs[r][i % 32] = (row0 + r < row_end && k < a.k) ? e4m3_value(A[(size_t)(row0 + r - shift) * ld + k]) : 0.f;
-      }
-      for (int b = 0; b < NB; ++b) {
-        const uint8_t* W = sh ? (b ? a.sb2.q : a.sb.q) : (b ? a.b2.q : a.b.q) + (size_t)g * a.nout * a.k;
-        for (int i = threadIdx.x; i < 128 * 32; i += 256) {
-          const int n = i / 32, k = k0 + i % 32;
-          ws[b][n][i % 32] = (n0 + n < a.nout && k < a.k) ? e4m3_value(W[(size_t)(n0 + n) * a.k + k]) : 0.f;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int first = (int)cluster_index(), step = (int)cluster_count();
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t smem_base = smem_u32(smem);
+  float* scale_ring = reinterpret_cast<float*>(smem + F_STAGES * F_STAGE_BYTES);  // [F_SLOTS][MATS][2][128]
+
+  const int G = args.groups;
+  for (int i = threadIdx.x; i <= G; i += blockDim.x)
+    offs_sh[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.max_rows);
+  if constexpr (SWIGLU)
+    for (int i = threadIdx.x; i < F_CHUNK; i += blockDim.x) amax_sh[i] = 0u;
+  if (threadIdx.x == 0) abort_flag = 0;
+  __syncthreads();
+  if (warp == 0) f8_prefix(offs_sh, prefix_sh, G, args.n_o);
+  if (threadIdx.x == 32) {
+    for (int s = 0; s < F_STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tempty_bar[b], 2 * F_EPI_WARPS);
+      mbar_init(&peer_bar[b], 1);
+    }
+    for (int s = 0; s < F_SLOTS; ++s) {
+      mbar_init(&sfull_bar[s], 1);
+      mbar_init(&sempty_bar[s], F_EPI_WARPS);
+    }
+    mbar_init(&amax_bar, F_EPI_WARPS);
+    mbar_init(&inv_bar, F_EPI_WARPS);
+    for (int j = 0; j < F_TRING; ++j) {
+      mbar_init(&tr_full[j], 1);
+      mbar_init(&tr_empty[j], F_TRING_READERS);
+    }
+    mbar_init(&drain_bar, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_sh)),
+                 "r"(TC_TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before either signals the other
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_sh;
+  const int total_tiles = prefix_sh[G];
+  const int nk = args.nk;
+  const int n_stage_tiles = (nk + F_KB - 1) / F_KB;  // stages per tile
+
+  // the next published tile index, for a role of one warp (every lane calls) or one thread
+  auto take_warp = [&](int& rs, uint32_t& rph, int& t) -> bool {
+    if (!f8_warp_wait<true>(&tr_full[rs], rph, args, &abort_flag, F_SITE_RING)) return false;
+    t = tile_ring[rs];
+    const uint32_t z = depend_zero((uint32_t)t);  // every lane's read has returned ...
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(&tr_empty[rs], 0) + z);  // ... before the slot is freed
+    if (++rs == F_TRING) {
+      rs = 0;
+      rph ^= 1u;
+    }
+    return true;
+  };
+
+  if (warp < F_EPI_WARP0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0) {
+      // ======================= TMA producer (both CTAs) =======================
+      if (lane == 0) {
+        tma_prefetch_map(&maps.w);
+        int stage = 0;
+        uint32_t phase = 0;
+        long issued = 0;
+        bool ok = true;
+        // The even CTA's producer claims tiles and publishes their indices (and
+        // finally one past the last) to every role of both CTAs; a tile's
+        // successor is published right after the tile's first stage is issued.
+        int rs = 0;
+        uint32_t rph = 0;
+        auto publish = [&](int v) -> bool {
+          if (!f8_wait<true>(&tr_empty[rs], rph ^ 1u, args, &abort_flag, F_SITE_RING)) return false;
+          tile_ring[rs] = v;
+          mbar_arrive(&tr_full[rs]);
+          const uint32_t peer_full = map_to_rank(&tr_full[rs], 1);
+          mbar_arrive_expect_tx_cluster(peer_full, 4);
+          st_async_b32(map_to_rank((const void*)&tile_ring[rs], 1), (uint32_t)v, peer_full);
+          if (++rs == F_TRING) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          return true;
+        };
+        auto take = [&](int& v) -> bool {
+          if (!f8_wait<true>(&tr_full[rs], rph, args, &abort_flag, F_SITE_RING)) return false;
+          v = tile_ring[rs];
+          mbar_arrive_cluster_relaxed(map_to_rank(&tr_empty[rs], 0) + depend_zero((uint32_t)v));
+          if (++rs == F_TRING) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          return true;
+        };
+        auto claim = [&]() -> int { return step + atomicAdd(args.hdr + F_CLAIM_WORD, 1); };
+        int t = first;
+        int pending = 0;  // even CTA: the claimed successor of the next tile
+        if (leader) {
+          ok = publish(t);
+          if (ok && t < total_tiles) pending = claim();
+        } else {
+          ok = take(t);
+        }
+        while (ok && t < total_tiles) {
+          const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+          const bool sh = tl.group == args.shared_group;
+          const CUtensorMap* wm = sh ? &maps.ws : &maps.w;
+          const bool own_rows = sh && args.shared_a;
+          const int half = tl.n >> 1;  // rows of the chunk in each CTA (8 .. 128)
+          const CUtensorMap* xm = own_rows ? &maps.xs[half / 8 - 1] : &maps.x[half / 8 - 1];
+          const int x_row = (own_rows ? tl.row0 - offs_sh[tl.group] : tl.row0) + (int)rank * half;
+          const int w_base = sh ? 0 : tl.group * args.nout;
+          const int w_row = SWIGLU ? (w_base + tl.o * 128 + (int)rank * 64) / 8 : w_base + tl.o * 256 + (int)rank * 128;
+          const uint32_t x_kblk = (uint32_t)(half * F_BK);
+          int next = 0;
+          bool sent = !leader;
+          for (int ks = 0; ks < n_stage_tiles; ++ks) {
+            if (!f8_wait<false>(&empty_bar[stage], phase ^ 1u, args, &abort_flag, SITE_EMPTY)) {
+              ok = false;
+              break;
+            }
+            const uint32_t sa = smem_base + stage * F_STAGE_BYTES;
+            const uint32_t full_leader = map_to_rank(&full_bar[stage], 0);
+            // a view load brings F_KB k-blocks (zeros past K), else one load per k-block
+            const int kb_n = args.view ? F_KB : min(F_KB, nk - ks * F_KB);
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2u * (uint32_t)kb_n * (F_KBLK_BYTES + x_kblk));
+            if (args.view) {
+              if (SWIGLU) f8_load_5d(sa, wm, full_leader, w_row, ks * F_KB);
+              else f8_load_3d(sa, wm, full_leader, 0, w_row, ks * F_KB);
+              f8_load_3d(sa + F_A_BYTES, xm, full_leader, 0, x_row, ks * F_KB);
+            } else {
+              for (int j = 0; j < kb_n; ++j) {
+                const int c0 = (ks * F_KB + j) * F_BK;
+                if (SWIGLU) f8_load_4d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
+                else f8_load_2d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
+                f8_load_2d(sa + F_A_BYTES + j * x_kblk, xm, full_leader, c0, x_row);
+              }
+            }
+            ++issued;
+            if (++stage == F_STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (!sent) {
+              sent = true;
+              next = pending;
+              if (!publish(next)) {
+                ok = false;
+                break;
+              }
+              if (next < total_tiles) pending = claim();
+            }
+          }
+          if (!ok) break;
+          if (leader) {
+            t = next;
+          } else if (!take(t)) {
+            break;
+          }
+        }
+        // Drain (even CTA, which owns the full barriers): the last loads of
+        // both CTAs have landed before exit.
+        if (leader) {
+          const long n_drain = issued < F_STAGES ? issued : F_STAGES;
+          int s = stage;
+          uint32_t ph = phase;
+          for (long i = 0; i < n_drain; ++i) {
+            if (--s < 0) {
+              s = F_STAGES - 1;
+              ph ^= 1u;
+            }
+            mbar_wait_bounded(&full_bar[s], ph, args.wait_ns, nullptr, args.hdr, KID_GEMM_FP8, SITE_DRAIN);
+          }
+          // every pair has made its last claim before the last one to get here
+          // clears the counter for the next launch
+          __threadfence();
+          if (atomicAdd(args.hdr + F_DONE_WORD, 1) == step - 1) {
+            atomicExch(args.hdr + F_CLAIM_WORD, 0);
+            atomicExch(args.hdr + F_DONE_WORD, 0);
+          }
         }
       }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int b = 0; b < NB; ++b)
-          for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j)
-              in[b][i][j] = fmaf(xs[warp * 4 + i][k], ws[b][lane + 32 * j][k], in[b][i][j]);
-    }
-    for (int b = 0; b < NB; ++b) {
-      const float* S = sh ? (b ? a.sb2.scale : a.sb.scale) : (b ? a.b2.scale : a.b.scale) + (size_t)g * nnb * nkb;
-      const float sb = S[(size_t)blockIdx.x * nkb + kb];
-      for (int i = 0; i < 4; ++i) {
-        const int r = row0 + warp * 4 + i;
-        if (r >= row_end) continue;
-        const float s = As[(size_t)(r - shift) * nkb + kb] * sb;
-        for (int j = 0; j < 4; ++j) acc[b][i][j] = fmaf(in[b][i][j], s, acc[b][i][j]);
+    } else if (warp == 1) {
+      // ======================= MMA issuer (even CTA) =======================
+      if (leader && lane == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        int buf = 0;
+        uint32_t bphase = 0;
+        bool ok = true;
+        int rs = 0;
+        uint32_t rph = 0;
+        while (ok) {
+          if (!f8_wait<true>(&tr_full[rs], rph, args, &abort_flag, F_SITE_RING)) break;
+          const int t = tile_ring[rs];
+          mbar_arrive(&tr_empty[rs]);
+          if (++rs == F_TRING) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          if (t >= total_tiles) break;
+          const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+          const uint32_t idesc = f8_idesc(256, tl.n);
+          const uint32_t x_kblk = (uint32_t)((tl.n >> 1) * F_BK);
+          for (int ks = 0; ks < n_stage_tiles && ok; ++ks) {
+            if (!f8_wait<false>(&full_bar[stage], phase, args, &abort_flag, SITE_FULL)) {
+              ok = false;
+              break;
+            }
+            const uint32_t sa = smem_base + stage * F_STAGE_BYTES;
+            const int kb_n = min(F_KB, nk - ks * F_KB);
+            for (int j = 0; j < kb_n; ++j) {
+              if (!f8_wait<true>(&tempty_bar[buf], bphase ^ 1u, args, &abort_flag, SITE_TMEM_EMPTY)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t d_tmem = tmem_base + (uint32_t)(buf * 256);
+              const uint64_t adesc = sw128_desc(sa + (uint32_t)(j * F_KBLK_BYTES));
+              const uint64_t bdesc = sw128_desc(sa + F_A_BYTES + (uint32_t)j * x_kblk);
+#pragma unroll
+              for (int kk = 0; kk < F_BK / 32; ++kk)  // K = 32 per MMA: 32 bytes further along the row
+                f8_mma(d_tmem, adesc + (uint64_t)(kk * 2), bdesc + (uint64_t)(kk * 2), idesc, kk != 0);
+              tc2_commit_both(&tfull_bar[buf]);
+              buf ^= 1;
+              if (buf == 0) bphase ^= 1u;
+            }
+            if (!ok) break;
+            tc2_commit_both(&empty_bar[stage]);
+            if (++stage == F_STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // Drain: every MMA issued here completes before TMEM is freed and
+        // before the odd CTA (whose shared memory they read) may exit.
+        tc2_commit_own(&drain_bar);
+        mbar_wait_bounded(&drain_bar, 0, args.wait_ns, nullptr, args.hdr, KID_GEMM_FP8, SITE_DRAIN);
       }
-    }
-  }
-  for (int i = 0; i < 4; ++i) {
-    const int r = row0 + warp * 4 + i;
-    if (EPI == moe_host::EPI_SWIGLU) {
-      float v[4], m = 0.f;
-      for (int j = 0; j < 4; ++j) {
-        v[j] = n0 + lane + 32 * j < a.nout ? silu_f(acc[0][i][j]) * acc[NB - 1][i][j] : 0.f;
-        m = fmaxf(m, fabsf(v[j]));
-      }
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float sc = quant_scale(m), inv = __frcp_rn(sc);
-      if (r >= row_end) continue;
-      for (int j = 0; j < 4; ++j)
-        if (n0 + lane + 32 * j < a.nout) ((uint8_t*)a.c)[(size_t)r * a.nout + n0 + lane + 32 * j] = e4m3x1(v[j] * inv);
-      if (lane == 0) a.c_scale[(size_t)r * nnb + blockIdx.x] = sc;
     } else {
-      if (r >= row_end) continue;
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + lane + 32 * j;
-        if (n >= a.nout) continue;
-        if (EPI == moe_host::EPI_F32) ((float*)a.c)[(size_t)r * a.nout + n] = acc[0][i][j];
-        else ((bf16*)a.c)[(size_t)r * a.nout + n] = __float2bfloat16_rn(acc[0][i][j]);
+      // ======================= scale products (warps 2, 3) =======================
+      int rs = 0, t;
+      uint32_t rph = 0;
+      uint32_t kc = 0;  // k-blocks of all tiles so far: slot kc % F_SLOTS, warp kc % 2
+      const int nkb = nk;
+      bool ok = true;
+      while (ok && take_warp(rs, rph, t) && t < total_tiles) {
+        const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+        const bool sh = tl.group == args.shared_group;
+        const bool own_rows = sh && args.shared_a;
+        const float* as = own_rows ? args.sas + (size_t)(tl.row0 - offs_sh[tl.group]) * nkb
+                                   : args.as + (size_t)tl.row0 * nkb;
+        const int nb = SWIGLU ? tl.o : min(2 * tl.o + (int)rank, args.nnb - 1);
+        const size_t b_at = ((size_t)(sh ? 0 : tl.group) * args.nnb + nb) * nkb;
+        const float* b0 = (sh ? args.sbs[0] : args.bs[0]) + b_at;
+        const float* b1 = (sh ? args.sbs[MATS - 1] : args.bs[MATS - 1]) + b_at;
+        const int cw = tl.n >> 1;
+        float cur[8], cur_b[2];
+        auto load = [&](int kb, float (&v)[8], float (&b)[2]) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = lane + 32 * i;
+            v[i] = r < tl.rows ? __ldg(as + (size_t)r * nkb + kb) : 0.f;
+          }
+          b[0] = __ldg(b0 + kb);
+          b[1] = MATS == 2 ? __ldg(b1 + kb) : 0.f;
+        };
+        const int kb0 = (int)((kc ^ (uint32_t)warp) & 1u);  // this warp's first k-block of the tile
+        if (kb0 < nk) load(kb0, cur, cur_b);
+        for (int kb = kb0; kb < nk; kb += 2) {
+          float nxt[8], nxt_b[2];
+          if (kb + 2 < nk) load(kb + 2, nxt, nxt_b);
+          const uint32_t n = kc + (uint32_t)kb;
+          const int slot = (int)(n % F_SLOTS);
+          if (!f8_warp_wait<false>(&sempty_bar[slot], ((n / F_SLOTS) & 1u) ^ 1u, args, &abort_flag, F_SITE_SCALE)) {
+            ok = false;
+            break;
+          }
+          float* dst = scale_ring + slot * (MATS * F_CHUNK);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = lane + 32 * i;
+            if (r < tl.n) {
+              const int at = r < cw ? f8_scale_at(r) : 128 + f8_scale_at(r - cw);
+#pragma unroll
+              for (int m = 0; m < MATS; ++m) dst[m * F_CHUNK + at] = __fmul_rn(cur[i], cur_b[m]);
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull_bar[slot]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
+          cur_b[0] = nxt_b[0];
+          cur_b[1] = nxt_b[1];
+        }
+        kc += (uint32_t)nk;
+      }
+    }
+  } else {
+    // ======================= epilogue (warps 4..11, both CTAs) =======================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3;               // TMEM lanes 32 * quarter .. + 31
+    const int hf = (warp - F_EPI_WARP0) >> 2;   // half of the chunk's columns
+    const int owner = threadIdx.x - F_EPI_WARP0 * 32;  // SwiGLU: the row whose scale this thread makes
+    const uint32_t peer = rank ^ 1u;
+    int buf = 0;
+    uint32_t bphase = 0, kc = 0, tiles_done = 0;
+    int rs = 0, t;
+    uint32_t rph = 0;
+    bool ok = true;
+    while (ok && take_warp(rs, rph, t) && t < total_tiles) {
+      const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+      const int cw = tl.n >> 1;  // columns of this warp: hf * cw .. + cw - 1
+      uint64_t acc[4][2][4][2];  // [32 columns][16 lanes][8 columns][rows l / 4, + 8]: pairs of columns
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[b][i >> 3][(i >> 1) & 3][i & 1] = 0ull;
+      for (int kb = 0; kb < nk; ++kb, ++kc) {
+        const int slot = (int)(kc % F_SLOTS);
+        if (!f8_warp_wait<false>(&sfull_bar[slot], (kc / F_SLOTS) & 1u, args, &abort_flag, F_SITE_SCALE) ||
+            !f8_warp_wait<false>(&tfull_bar[buf], bphase, args, &abort_flag, SITE_TMEM_FULL)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256 + hf * cw);
+        const float* sc = scale_ring + slot * (MATS * F_CHUNK) + hf * 128 + (lane & 3) * 4;
+        uint32_t v[2][2][16];
+        MOE_TMEM_LD16x32(tb, v[0][0]);
+        MOE_TMEM_LD16x32(tb + (16u << 16), v[0][1]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b * 32 < cw) {
+            MOE_TMEM_WAIT16(v[b & 1][0]);
+            MOE_TMEM_WAIT16(v[b & 1][1]);
+            if (b < 3 && (b + 1) * 32 < cw) {
+              MOE_TMEM_LD16x32(tb + (uint32_t)(b + 1) * 32u, v[(b + 1) & 1][0]);
+              MOE_TMEM_LD16x32(tb + (uint32_t)(b + 1) * 32u + (16u << 16), v[(b + 1) & 1][1]);
+            } else {
+              // the accumulator has been read: its slot may be overwritten
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(&tempty_bar[buf], 0));
+            }
+#pragma unroll
+            for (int jj = 0; jj < 2; ++jj) {
+              ulonglong2 s[2];
+              s[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 32 + jj * 16);
+              s[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 32 + jj * 16) : s[0];
+#pragma unroll
+              for (int l16 = 0; l16 < 2; ++l16)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t* p = &v[b & 1][l16][jj * 8 + 2 * h];
+                  fma2(acc[b][l16][2 * jj][h], pack64(p[0], p[1]), s[h].x);
+                  fma2(acc[b][l16][2 * jj + 1][h], pack64(p[4], p[5]), s[h].y);
+                }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty_bar[slot]);
+        buf ^= 1;
+        if (buf == 0) bphase ^= 1u;
+      }
+      if (!ok) break;
+
+      const int c_lane = 2 * (lane & 3);  // this lane's first column of every eight
+      const int valid = tl.rows - hf * cw;  // rows of this half that exist
+      const size_t row0 = (size_t)tl.row0 + hf * cw;
+      if constexpr (EPI == moe_host::EPI_F32) {
+        const int n_base = tl.o * 256 + (int)rank * 128 + quarter * 32 + (lane >> 2);
+        float* C = reinterpret_cast<float*>(args.c);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = b * 32 + j * 8 + c_lane, n = n_base + 8 * i;
+              const float2 f = unpack64(acc[b][i >> 1][j][i & 1]);
+              if (n < args.nout) {
+                if (r < valid && r < cw) C[(row0 + r) * args.nout + n] = f.x;
+                if (r + 1 < valid && r + 1 < cw) C[(row0 + r + 1) * args.nout + n] = f.y;
+              }
+            }
+      } else if constexpr (EPI == moe_host::EPI_STORE) {
+        // 16 rows x 32 columns at a time through this warp's block of shared memory
+        uint8_t* stage = smem + F_STAGES * F_STAGE_BYTES + F_SLOTS * MATS * F_CHUNK * 4 +
+                         (warp - F_EPI_WARP0) * F_OUT_BYTES;
+        const uint32_t st_at = smem_u32(stage) + (uint32_t)((lane & 7) * F_OUT_PITCH + (lane >> 3) * 16);
+        const int n0 = tl.o * 256 + (int)rank * 128 + quarter * 32;
+        bf16* C = reinterpret_cast<bf16*>(args.c);
+        const int left = min(valid, cw);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int r0 = b * 32 + jj * 16;
+            if (r0 >= left) continue;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t p[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack64(acc[b][i >> 1][2 * jj + j][i & 1]);
+                p[i] = pack_bf16x2(f.x, f.y);
+              }
+              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                               st_at + (uint32_t)(j * 8 * F_OUT_PITCH)),
+                           "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                           : "memory");
+            }
+            __syncwarp();
+            if (args.vec) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int r = i * 8 + (lane >> 2), n = n0 + (lane & 3) * 8;
+                const uint4 w = *reinterpret_cast<const uint4*>(stage + r * F_OUT_PITCH + (lane & 3) * 16);
+                if (r0 + r < left && n < args.nout) *reinterpret_cast<uint4*>(C + (row0 + r0 + r) * args.nout + n) = w;
+              }
+            } else {
+              for (int r = 0; r < 16 && r0 + r < left; ++r)
+                if (n0 + lane < args.nout)
+                  C[(row0 + r0 + r) * args.nout + n0 + lane] =
+                      *reinterpret_cast<const bf16*>(stage + r * F_OUT_PITCH + lane * 2);
+            }
+          }
+      } else {
+        const int unit0 = tl.o * 128 + (int)rank * 64 + quarter * 16;  // hidden units of this warp
+        const bool up_first = tl.group == args.shared_group ? args.s_up_first : args.up_first;
+        // the activation in place: acc[..][0] holds its pair of rows
+        float m[32];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float mx = 0.f, my = 0.f;
+            if (b * 32 < cw) {
+#pragma unroll
+              for (int l16 = 0; l16 < 2; ++l16) {
+                const float2 p = unpack64(acc[b][l16][j][0]), q = unpack64(acc[b][l16][j][1]);
+                const bool in = unit0 + l16 * 8 + (lane >> 2) < args.nout;
+                const float vx = in ? __fmul_rn(f8_silu(up_first ? q.x : p.x), up_first ? p.x : q.x) : 0.f;
+                const float vy = in ? __fmul_rn(f8_silu(up_first ? q.y : p.y), up_first ? p.y : q.y) : 0.f;
+                mx = fmaxf(mx, fabsf(vx));
+                my = fmaxf(my, fabsf(vy));
+                acc[b][l16][j][0] = pack64(__float_as_uint(vx), __float_as_uint(vy));
+              }
+            }
+            m[b * 8 + j * 2] = mx;
+            m[b * 8 + j * 2 + 1] = my;
+          }
+        // each row's largest magnitude over the 8 lanes that share its column: a
+        // reduce-scatter, after which a lane holds 4 of the 32 rows
+#pragma unroll
+        for (int o = 16, n = 16; o >= 4; o >>= 1, n >>= 1) {
+          const bool upper = lane & o;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const float give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+            m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+          }
+        }
+        const int i0 = ((lane & 16) ? 16 : 0) + ((lane & 8) ? 8 : 0) + ((lane & 4) ? 4 : 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = i0 + i;  // b * 8 + j * 2 + e
+          const int c = (at >> 1) * 8 + c_lane + (at & 1);
+          if (c < cw) atomicMax(&amax_sh[hf * cw + c], __float_as_uint(m[i]));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&amax_bar);
+        const uint32_t once = tiles_done & 1u;          // phase of the barriers used once per tile
+        const uint32_t pb = tiles_done & 1u, pph = (tiles_done >> 1) & 1u;
+        if (!f8_warp_wait<false>(&amax_bar, once, args, &abort_flag, F_SITE_AMAX)) break;
+        // one thread per row: trade the magnitude with the other CTA, make the scale
+        if (owner == 0) mbar_arrive_expect_tx(&peer_bar[pb], (uint32_t)tl.n * 4u);
+        unsigned mine = 0u;
+        if (owner < tl.n) {
+          mine = amax_sh[owner];
+          amax_sh[owner] = 0u;
+          st_async_b32(map_to_rank((const void*)&peer_sh[pb][owner], peer), mine, map_to_rank(&peer_bar[pb], peer));
+        }
+        if (!f8_warp_wait<true>(&peer_bar[pb], pph, args, &abort_flag, F_SITE_AMAX)) break;
+        if (owner < tl.n) {
+          const float scale = quant_scale(fmaxf(__uint_as_float(mine), peer_sh[pb][owner]));
+          inv_sh[owner < cw ? f8_scale_at(owner) : 128 + f8_scale_at(owner - cw)] = __frcp_rn(scale);
+          if (leader && owner < tl.rows) args.c_scale[(size_t)(tl.row0 + owner) * args.n_o + tl.o] = scale;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&inv_bar);
+        if (!f8_warp_wait<false>(&inv_bar, once, args, &abort_flag, F_SITE_AMAX)) break;
+        ++tiles_done;
+        // codes: four consecutive units of one row per lane, 16 bytes of eight rows per store
+        uint8_t* C = reinterpret_cast<uint8_t*>(args.c);
+        const int item = (lane >> 2) & 3;  // (16-lane half, row of the pair) this lane stores
+        const int unit = unit0 + (item >> 1) * 8 + (lane >> 4) * 4;
+        const int left = min(valid, cw);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (b * 32 >= cw) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 inv = *reinterpret_cast<const float2*>(inv_sh + hf * 128 + b * 32 + (j >> 1) * 16 +
+                                                                (lane & 3) * 4 + (j & 1) * 2);
+            const float2 lo = unpack64(acc[b][0][j][0]), hi = unpack64(acc[b][1][j][0]);
+            const uint32_t w = f8_transpose_bytes(e4m3x4(lo.x * inv.x, lo.y * inv.y, hi.x * inv.x, hi.y * inv.y));
+            const int r = b * 32 + j * 8 + c_lane + (item & 1);
+            if (r < left && unit < args.nout) *reinterpret_cast<uint32_t*>(C + (row0 + r) * args.nout + unit) = w;
+          }
+        }
       }
     }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(TC_TMEM_COLS)
+                 : "memory");
 }
 
 }  // namespace moe
 
 namespace moe_host {
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();  // gemm_tc.cu
+
+// Tensor map of bytes: dims and strides (of dims 1 ..) as given, 128-byte
+// swizzle, zero fill outside.
+static bool byte_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                     const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return false;
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A row-major [rows][k] matrix, rows ld bytes apart, in boxes of box_rows rows x
+// 128 columns; as a view {128, rows, k / 128} the box also spans two k-blocks.
+static bool rows_map(CUtensorMap* m, const void* base, int64_t rows, int k, int64_t ld, int box_rows, bool view) {
+  if (view) {
+    const cuuint64_t dims[3] = {128, (cuuint64_t)rows, (cuuint64_t)(k / 128)}, strides[2] = {(cuuint64_t)ld, 128};
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, moe::F_KB};
+    return byte_map(m, base, 3, dims, strides, box);
+  }
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld};
+  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  return byte_map(m, base, 2, dims, strides, box);
+}
+
+// Two [rows][k] matrices `apart` bytes from each other, interleaved by eight
+// rows: boxes of eight such groups of each (128 rows).  rows % 8 == 0.
+static bool interleaved_map(CUtensorMap* m, const void* low, int64_t apart, int64_t rows, int k, bool view) {
+  const cuuint64_t K = (cuuint64_t)k;
+  if (view) {
+    const cuuint64_t dims[5] = {128, 8, 2, (cuuint64_t)(rows / 8), K / 128};
+    const cuuint64_t strides[4] = {K, (cuuint64_t)apart, 8 * K, 128};
+    const cuuint32_t box[5] = {128, 8, 2, 8, moe::F_KB};
+    return byte_map(m, low, 5, dims, strides, box);
+  }
+  const cuuint64_t dims[4] = {K, 8, 2, (cuuint64_t)(rows / 8)}, strides[3] = {K, (cuuint64_t)apart, 8 * K};
+  const cuuint32_t box[4] = {128, 8, 2, 8};
+  return byte_map(m, low, 4, dims, strides, box);
+}
+
+// Clusters of two that can be resident at once (one CTA per SM), per device.
+template <int EPI>
+static int f8_resident_pairs() {
+  static std::atomic<int> cache[64] = {};
+  const int dev = current_device();
+  if (dev >= 0 && dev < 64) {
+    const int c = cache[dev].load(std::memory_order_relaxed);
+    if (c > 0) return c;
+  }
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
+  cfg.blockDim = dim3(moe::F_THREADS);
+  cfg.dynamicSmemBytes = moe::f8_smem_bytes<EPI>();
+  if (cudaOccupancyMaxActiveClusters(&n, moe::gemm_fp8_kernel<EPI>, &cfg) != cudaSuccess || n <= 0) {
+    cudaGetLastError();
+    n = sm_count() / 2;
+  }
+  if (n > sm_count() / 2) n = sm_count() / 2;
+  if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+template <int EPI>
+static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound, cudaStream_t s) {
+  static SmemLimit lim;
+  const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI>, moe::f8_smem_bytes<EPI>(), lim);
+  if (st != MOE_OK) return st;
+  const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI>());
+  moe::gemm_fp8_kernel<EPI><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI>(), s>>>(maps, args);
+  return launch_status();
+}
+
+// Weight map(s) of one set of matrices; *up_first: the second lies lower in memory.
+static moe_status weight_map(CUtensorMap* m, int epi, const Fp8Operand& b, const Fp8Operand& b2, int64_t rows, int k,
+                             bool view, int* up_first) {
+  *up_first = 0;
+  if (epi != EPI_SWIGLU) return rows_map(m, b.q, rows, k, k, 128, view) ? MOE_OK : MOE_ERR_CUDA;
+  *up_first = b2.q < b.q;
+  const uint8_t* low = *up_first ? b2.q : b.q;
+  const int64_t apart = *up_first ? b.q - b2.q : b2.q - b.q;
+  if (apart == 0 || apart >= (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;  // a TMA stride has 40 bits
+  return interleaved_map(m, low, apart, rows, k, view) ? MOE_OK : MOE_ERR_CUDA;
+}
+
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.max_rows == 0) return MOE_OK;
-  const dim3 grid((unsigned)q_blocks(g.nout), (unsigned)((g.max_rows + 31) / 32 + (g.offsets ? g.groups : 0)));
-  moe::Fp8Args a;
-  a.g = g;
-  if (g.epi == EPI_SWIGLU) moe::gemm_fp8_simple_kernel<EPI_SWIGLU><<<grid, 256, 0, s>>>(a);
-  else if (g.epi == EPI_F32) moe::gemm_fp8_simple_kernel<EPI_F32><<<grid, 256, 0, s>>>(a);
-  else moe::gemm_fp8_simple_kernel<EPI_STORE><<<grid, 256, 0, s>>>(a);
-  return launch_status();
+  const bool swiglu = g.epi == EPI_SWIGLU;
+  const bool view = g.k % 128 == 0;
+  const bool shared = g.sb.q != nullptr && g.offsets != nullptr;
+  const bool shared_a = shared && g.sa.q != nullptr && g.sa_rows > 0;
+  moe::Fp8Maps maps;
+  moe::Fp8Args args;
+  const int64_t w_rows = std::max<int64_t>((int64_t)(shared ? g.groups - 1 : g.groups) * g.nout, 1);
+  moe_status st = weight_map(&maps.w, g.epi, g.b, g.b2, w_rows, g.k, view, &args.up_first);
+  if (st != MOE_OK) return st;
+  args.s_up_first = 0;
+  if (shared) {
+    st = weight_map(&maps.ws, g.epi, g.sb, g.sb2, g.nout, g.k, view, &args.s_up_first);
+    if (st != MOE_OK) return st;
+  }
+  // row boxes: only those that a chunk can take (one group: its two chunk sizes)
+  auto row_maps = [&](CUtensorMap* ms, const Fp8Operand& a, int64_t rows, bool one_group) -> bool {
+    const int64_t ch = (rows + moe::F_CHUNK - 1) / moe::F_CHUNK;
+    const int64_t nc = ((rows + ch - 1) / ch + 15) / 16 * 16;
+    const int64_t last = std::max<int64_t>(16, (rows - (ch - 1) * nc + 15) / 16 * 16);
+    const int64_t most = std::min<int64_t>(moe::F_CHUNK, (rows + 15) / 16 * 16);
+    for (int i = 0; i < moe::F_XMAPS; ++i) {
+      const int64_t n = 16 * (i + 1);
+      if (one_group ? (n == nc || n == last) : n <= most)
+        if (!rows_map(&ms[i], a.q, rows, g.k, a.ld, 8 * (i + 1), view)) return false;
+    }
+    return true;
+  };
+  const int64_t a_rows = shared_a ? std::max<int64_t>((int64_t)g.max_rows - g.sa_rows, 1) : g.max_rows;
+  if (!row_maps(maps.x, g.a, a_rows, g.offsets == nullptr)) return MOE_ERR_CUDA;
+  if (shared_a && !row_maps(maps.xs, g.sa, g.sa_rows, true)) return MOE_ERR_CUDA;
+  args.offsets = g.offsets;
+  args.groups = g.offsets ? g.groups : 1;
+  args.max_rows = g.max_rows;
+  args.nout = g.nout;
+  args.nk = q_blocks(g.k);
+  args.n_o = swiglu ? (g.nout + 127) / 128 : (g.nout + 255) / 256;
+  args.view = view ? 1 : 0;
+  args.nnb = q_blocks(g.nout);
+  args.as = g.a.scale;
+  args.sas = g.sa.scale;
+  for (int m = 0; m < 2; ++m) {
+    args.bs[m] = (swiglu && (m ^ args.up_first)) ? g.b2.scale : g.b.scale;
+    args.sbs[m] = (swiglu && (m ^ args.s_up_first)) ? g.sb2.scale : g.sb.scale;
+  }
+  args.c = g.c;
+  args.c_scale = g.c_scale;
+  args.vec = (g.nout % 8 == 0 && (uintptr_t)g.c % 16 == 0) ? 1 : 0;
+  args.shared_group = shared ? g.groups - 1 : -1;
+  args.shared_a = shared_a ? 1 : 0;
+  args.hdr = g.hdr;
+  args.wait_ns = wait_limit_ns();
+  // upper bound on the tiles; the exact count lives on the device
+  const int64_t chunks = (int64_t)(g.max_rows + moe::F_CHUNK - 1) / moe::F_CHUNK + (g.offsets ? args.groups : 0);
+  const int64_t bound = chunks * args.n_o;
+  if (swiglu) return launch_f8_t<EPI_SWIGLU>(maps, args, bound, s);
+  if (g.epi == EPI_F32) return launch_f8_t<EPI_F32>(maps, args, bound, s);
+  return launch_f8_t<EPI_STORE>(maps, args, bound, s);
 }
 
 }  // namespace moe_host
