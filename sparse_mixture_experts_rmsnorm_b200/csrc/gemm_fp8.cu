@@ -16,7 +16,9 @@
 // 16x256b shape (lane l holds rows l / 4 and l / 4 + 8, columns 2 (l % 4) and
 // + 1 of every eight), so one product sa * sb, read from shared memory, serves
 // four values.  Two warps beside the producer and the MMA issuer form those
-// products a few k-blocks ahead.
+// products, their inputs loaded two k-blocks ahead, and complete the same barrier
+// as the accumulator.  A warp loads the next 16 columns, across k-blocks too,
+// before it adds the last ones.
 //
 // Gate and up.  One 5-D view over both matrices (their distance is a stride)
 // interleaves them in shared memory, eight gate rows, eight up rows, so a
@@ -29,7 +31,7 @@
 //   warp 0      TMA producer in both CTAs; 3-stage ring of 64 KiB, two k-blocks
 //               per stage and (K % 128 == 0) one load per operand and stage;
 //   warp 1      TMEM allocation; in the even CTA lane 0 issues the MMAs;
-//   warps 2, 3  scale products, alternating k-blocks, into a ring of 4 slots;
+//   warps 2, 3  scale products, one warp per TMEM slot;
 //   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
 //               of the chunk's columns.
 // Tiles run group by group, a group's chunks in runs of eight per weight tile,
@@ -41,6 +43,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_fp8_kernels.h"
 #include "quant_common.cuh"
@@ -60,7 +63,7 @@ constexpr int F_CHUNK = 256;                          // most rows of a group in
 constexpr int F_RUN = 8;                              // chunks that walk a group's weight tiles together
 constexpr int F_XMAPS = 16;                           // row boxes of 8, 16, ..., 128 rows
 constexpr int F_TRING = 8;
-constexpr int F_SLOTS = 4;                            // k-blocks of scale products ahead
+constexpr int F_SLOTS = 2;                            // rows of scale products, one per TMEM slot
 // readers of a published tile index: even CTA: MMA thread, 2 scale and 8 epilogue
 // warps; odd CTA: producer, 2 and 8
 constexpr int F_TRING_READERS = 22;
@@ -192,7 +195,9 @@ __device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, const Fp
 template <bool CLUSTER>
 __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, const Fp8Args& a, volatile int* abort,
                                              int site) {
-  const bool ok = f8_wait<CLUSTER>(bar, parity, a, abort, site);
+  bool ok = CLUSTER ? f8_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  if (__builtin_expect(__all_sync(0xffffffffu, ok), 1)) return true;
+  ok = f8_wait<CLUSTER>(bar, parity, a, abort, site);
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -238,24 +243,20 @@ constexpr uint32_t f8_idesc(int m, int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// 16 TMEM lanes x 32 columns: register 4 j + i of lane l holds row l / 4 + 8 (i / 2),
+// 16 TMEM lanes x 16 columns: register 4 j + i of lane l holds row l / 4 + 8 (i / 2),
 // column 8 j + 2 (l % 4) + i % 2.
-#define MOE_TMEM_LD16x32(taddr, r)                                                                                  \
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "   \
-               "%13, %14, %15}, [%16];"                                                                             \
+#define MOE_TMEM_LD16x16(taddr, r)                                                                                 \
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"                    \
                : "=r"((r)[0]), "=r"((r)[1]), "=r"((r)[2]), "=r"((r)[3]), "=r"((r)[4]), "=r"((r)[5]), "=r"((r)[6]), \
-                 "=r"((r)[7]), "=r"((r)[8]), "=r"((r)[9]), "=r"((r)[10]), "=r"((r)[11]), "=r"((r)[12]),             \
-                 "=r"((r)[13]), "=r"((r)[14]), "=r"((r)[15])                                                        \
+                 "=r"((r)[7])                                                                                      \
                : "r"(taddr))
 
 // Waits for this thread's TMEM loads; the registers pass through it, so no use of them can move above it.
-#define MOE_TMEM_WAIT16(r)                                                                                          \
-  asm volatile("tcgen05.wait::ld.sync.aligned;"                                                                     \
-               : "+r"((r)[0]), "+r"((r)[1]), "+r"((r)[2]), "+r"((r)[3]), "+r"((r)[4]), "+r"((r)[5]), "+r"((r)[6]), \
-                 "+r"((r)[7]), "+r"((r)[8]), "+r"((r)[9]), "+r"((r)[10]), "+r"((r)[11]), "+r"((r)[12]),             \
-                 "+r"((r)[13]), "+r"((r)[14]), "+r"((r)[15])                                                        \
-               :                                                                                                    \
-               : "memory")
+__device__ __forceinline__ void f8_tmem_wait(uint32_t (&v)[2][8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(v[i >> 3][i & 7]));
+}
 
 __device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
   uint64_t v;
@@ -293,6 +294,80 @@ __device__ __forceinline__ uint32_t f8_transpose_bytes(uint32_t w) {
   return b0 ? __byte_perm(w, p, 0x3715) : __byte_perm(w, p, 0x6240);
 }
 
+// What the main loop of an epilogue warp needs, set up once.
+struct Fp8Drain {
+  uint32_t tmem;            // this warp's lanes of slot 0
+  uint32_t tempty_remote;   // the even CTA's tempty_bar[0]
+  uint64_t *tfull, *sempty; // this CTA's barriers of slot 0
+  const float* scales;      // this lane's first scale product of slot 0
+  uint32_t phase;           // of the next k-block's tfull
+  int slot;                 // ... and its slot
+};
+
+// Adds the k-blocks of one tile to acc[16 columns][16 lanes][8 columns][rows
+// l / 4, + 8] (pairs of columns).  NB batches of 16 columns from column col0 of
+// the slot.  Every lane calls it; false after a failed wait.
+template <int NB, int MATS>
+__device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Drain& d, int col0, int nk,
+                                              const Fp8Args& args, volatile int* abort) {
+  uint32_t v[2][2][8];
+  auto load = [&](int slot, int b, uint32_t (&r)[2][8]) {
+    const uint32_t at = d.tmem + (uint32_t)(slot * 256 + col0 + b * 16);
+    MOE_TMEM_LD16x16(at, r[0]);
+    MOE_TMEM_LD16x16(at + (16u << 16), r[1]);
+  };
+  auto wait_full = [&]() -> bool {
+    if (!f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL)) return false;
+    tc_fence_after();
+    return true;
+  };
+  if (!wait_full()) return false;
+  load(d.slot, 0, v[0]);
+  // one k-block whose first batch is on its way into v[P]
+  auto step = [&](auto first, bool more) -> bool {
+    constexpr int P = decltype(first)::value;
+    const int slot = d.slot;
+    const float* sc = d.scales + slot * (MATS * F_CHUNK);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint32_t(&r)[2][8] = v[(P + b) & 1];
+      f8_tmem_wait(r);
+      if (b + 1 < NB) load(slot, b + 1, v[(P + b + 1) & 1]);
+      ulonglong2 s[2];
+      s[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 16);
+      s[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 16) : s[0];
+      if (b + 1 == NB) {
+        // the slot's accumulator and scale products have been read
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) {
+          mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)slot * 8u);
+          mbar_arrive(d.sempty + slot);
+        }
+        d.slot ^= 1;
+        if (d.slot == 0) d.phase ^= 1u;
+        if (more) {
+          if (!wait_full()) return false;
+          load(d.slot, 0, v[(P + b + 1) & 1]);
+        }
+      }
+#pragma unroll
+      for (int l16 = 0; l16 < 2; ++l16)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          fma2(acc[b][l16][0][h], pack64(r[l16][2 * h], r[l16][2 * h + 1]), s[h].x);
+          fma2(acc[b][l16][1][h], pack64(r[l16][4 + 2 * h], r[l16][5 + 2 * h]), s[h].y);
+        }
+    }
+    return true;
+  };
+  for (int kb = 0; kb < nk; kb += 2) {
+    if (!step(std::integral_constant<int, 0>(), kb + 1 < nk)) return false;
+    if (kb + 1 < nk && !step(std::integral_constant<int, NB & 1>(), kb + 2 < nk)) return false;
+  }
+  return true;
+}
+
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args args) {
@@ -303,8 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   __shared__ __align__(8) uint64_t empty_bar[F_STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];        // used in the even CTA
-  __shared__ __align__(8) uint64_t sfull_bar[F_SLOTS];   // scale products of a k-block
-  __shared__ __align__(8) uint64_t sempty_bar[F_SLOTS];
+  __shared__ __align__(8) uint64_t sempty_bar[F_SLOTS];  // the slot's scale products have been read
   __shared__ __align__(8) uint64_t amax_bar;             // SwiGLU: every warp's magnitudes are in amax_sh
   __shared__ __align__(8) uint64_t peer_bar[2];          //         the other CTA's have arrived
   __shared__ __align__(8) uint64_t inv_bar;              //         1 / scale of every row is in inv_sh
@@ -342,13 +416,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       mbar_init(&empty_bar[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&tfull_bar[b], 1);
+      mbar_init(&tfull_bar[b], 2);  // the MMA's commit and the slot's scale warp
       mbar_init(&tempty_bar[b], 2 * F_EPI_WARPS);
+      mbar_init(&sempty_bar[b], F_EPI_WARPS);
       mbar_init(&peer_bar[b], 1);
-    }
-    for (int s = 0; s < F_SLOTS; ++s) {
-      mbar_init(&sfull_bar[s], 1);
-      mbar_init(&sempty_bar[s], F_EPI_WARPS);
     }
     mbar_init(&amax_bar, F_EPI_WARPS);
     mbar_init(&inv_bar, F_EPI_WARPS);
@@ -390,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   };
 
   if (warp < F_EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ======================= TMA producer (both CTAs) =======================
       if (lane == 0) {
@@ -577,7 +648,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       // ======================= scale products (warps 2, 3) =======================
       int rs = 0, t;
       uint32_t rph = 0;
-      uint32_t kc = 0;  // k-blocks of all tiles so far: slot kc % F_SLOTS, warp kc % 2
+      const int slot = warp & 1;
+      uint32_t kc = 0, sphase = 0;  // k-blocks of all tiles so far: k-block kc is in TMEM slot kc % 2
       const int nkb = nk;
       bool ok = true;
       while (ok && take_warp(rs, rph, t) && t < total_tiles) {
@@ -606,12 +678,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         for (int kb = kb0; kb < nk; kb += 2) {
           float nxt[8], nxt_b[2];
           if (kb + 2 < nk) load(kb + 2, nxt, nxt_b);
-          const uint32_t n = kc + (uint32_t)kb;
-          const int slot = (int)(n % F_SLOTS);
-          if (!f8_warp_wait<false>(&sempty_bar[slot], ((n / F_SLOTS) & 1u) ^ 1u, args, &abort_flag, F_SITE_SCALE)) {
+          if (!f8_warp_wait<false>(&sempty_bar[slot], sphase ^ 1u, args, &abort_flag, F_SITE_SCALE)) {
             ok = false;
             break;
           }
+          sphase ^= 1u;
           float* dst = scale_ring + slot * (MATS * F_CHUNK);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -623,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull_bar[slot]);
+          if (lane == 0) mbar_arrive(&tfull_bar[slot]);
 #pragma unroll
           for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
           cur_b[0] = nxt_b[0];
@@ -634,72 +705,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     }
   } else {
     // ======================= epilogue (warps 4..11, both CTAs) =======================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int quarter = warp & 3;               // TMEM lanes 32 * quarter .. + 31
     const int hf = (warp - F_EPI_WARP0) >> 2;   // half of the chunk's columns
     const int owner = threadIdx.x - F_EPI_WARP0 * 32;  // SwiGLU: the row whose scale this thread makes
     const uint32_t peer = rank ^ 1u;
-    int buf = 0;
-    uint32_t bphase = 0, kc = 0, tiles_done = 0;
+    Fp8Drain drain;
+    drain.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16);
+    drain.tempty_remote = map_to_rank(&tempty_bar[0], 0);
+    drain.tfull = tfull_bar;
+    drain.sempty = sempty_bar;
+    drain.scales = scale_ring + hf * 128 + (lane & 3) * 4;
+    drain.phase = 0;
+    drain.slot = 0;
+    uint32_t tiles_done = 0;
     int rs = 0, t;
     uint32_t rph = 0;
     bool ok = true;
     while (ok && take_warp(rs, rph, t) && t < total_tiles) {
       const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
       const int cw = tl.n >> 1;  // columns of this warp: hf * cw .. + cw - 1
-      uint64_t acc[4][2][4][2];  // [32 columns][16 lanes][8 columns][rows l / 4, + 8]: pairs of columns
+      uint64_t acc[8][2][2][2];
 #pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[b][i >> 3][(i >> 1) & 3][i & 1] = 0ull;
-      for (int kb = 0; kb < nk; ++kb, ++kc) {
-        const int slot = (int)(kc % F_SLOTS);
-        if (!f8_warp_wait<false>(&sfull_bar[slot], (kc / F_SLOTS) & 1u, args, &abort_flag, F_SITE_SCALE) ||
-            !f8_warp_wait<false>(&tfull_bar[buf], bphase, args, &abort_flag, SITE_TMEM_FULL)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t tb = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256 + hf * cw);
-        const float* sc = scale_ring + slot * (MATS * F_CHUNK) + hf * 128 + (lane & 3) * 4;
-        uint32_t v[2][2][16];
-        MOE_TMEM_LD16x32(tb, v[0][0]);
-        MOE_TMEM_LD16x32(tb + (16u << 16), v[0][1]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (b * 32 < cw) {
-            MOE_TMEM_WAIT16(v[b & 1][0]);
-            MOE_TMEM_WAIT16(v[b & 1][1]);
-            if (b < 3 && (b + 1) * 32 < cw) {
-              MOE_TMEM_LD16x32(tb + (uint32_t)(b + 1) * 32u, v[(b + 1) & 1][0]);
-              MOE_TMEM_LD16x32(tb + (uint32_t)(b + 1) * 32u + (16u << 16), v[(b + 1) & 1][1]);
-            } else {
-              // the accumulator has been read: its slot may be overwritten
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(&tempty_bar[buf], 0));
-            }
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              ulonglong2 s[2];
-              s[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 32 + jj * 16);
-              s[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 32 + jj * 16) : s[0];
-#pragma unroll
-              for (int l16 = 0; l16 < 2; ++l16)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t* p = &v[b & 1][l16][jj * 8 + 2 * h];
-                  fma2(acc[b][l16][2 * jj][h], pack64(p[0], p[1]), s[h].x);
-                  fma2(acc[b][l16][2 * jj + 1][h], pack64(p[4], p[5]), s[h].y);
-                }
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sempty_bar[slot]);
-        buf ^= 1;
-        if (buf == 0) bphase ^= 1u;
-      }
+      for (int i = 0; i < 64; ++i) acc[i >> 3][(i >> 2) & 1][(i >> 1) & 1][i & 1] = 0ull;
+      // columns past cw in the last batches add up unused values
+      if (cw > 96) ok = f8_accumulate<8, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
+      else if (cw > 64) ok = f8_accumulate<6, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
+      else if (cw > 32) ok = f8_accumulate<4, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
+      else if (cw > 16) ok = f8_accumulate<2, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
+      else ok = f8_accumulate<1, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
       if (!ok) break;
 
       const int c_lane = 2 * (lane & 3);  // this lane's first column of every eight
@@ -709,12 +743,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int n_base = tl.o * 256 + (int)rank * 128 + quarter * 32 + (lane >> 2);
         float* C = reinterpret_cast<float*>(args.c);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 8; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const int r = b * 32 + j * 8 + c_lane, n = n_base + 8 * i;
+              const int r = b * 16 + j * 8 + c_lane, n = n_base + 8 * i;
               const float2 f = unpack64(acc[b][i >> 1][j][i & 1]);
               if (n < args.nout) {
                 if (r < valid && r < cw) C[(row0 + r) * args.nout + n] = f.x;
@@ -730,51 +764,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         bf16* C = reinterpret_cast<bf16*>(args.c);
         const int left = min(valid, cw);
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 8; ++b) {
+          const int r0 = b * 16;
+          if (r0 >= left) continue;
+          __syncwarp();
 #pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int r0 = b * 32 + jj * 16;
-            if (r0 >= left) continue;
-            __syncwarp();
+          for (int j = 0; j < 2; ++j) {
+            uint32_t p[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              uint32_t p[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack64(acc[b][i >> 1][2 * jj + j][i & 1]);
-                p[i] = pack_bf16x2(f.x, f.y);
-              }
-              asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                               st_at + (uint32_t)(j * 8 * F_OUT_PITCH)),
-                           "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
-                           : "memory");
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack64(acc[b][i >> 1][j][i & 1]);
+              p[i] = pack_bf16x2(f.x, f.y);
             }
-            __syncwarp();
-            if (args.vec) {
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int r = i * 8 + (lane >> 2), n = n0 + (lane & 3) * 8;
-                const uint4 w = *reinterpret_cast<const uint4*>(stage + r * F_OUT_PITCH + (lane & 3) * 16);
-                if (r0 + r < left && n < args.nout) *reinterpret_cast<uint4*>(C + (row0 + r0 + r) * args.nout + n) = w;
-              }
-            } else {
-              for (int r = 0; r < 16 && r0 + r < left; ++r)
-                if (n0 + lane < args.nout)
-                  C[(row0 + r0 + r) * args.nout + n0 + lane] =
-                      *reinterpret_cast<const bf16*>(stage + r * F_OUT_PITCH + lane * 2);
-            }
+            asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                             st_at + (uint32_t)(j * 8 * F_OUT_PITCH)),
+                         "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
+                         : "memory");
           }
+          __syncwarp();
+          if (args.vec) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = i * 8 + (lane >> 2), n = n0 + (lane & 3) * 8;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + r * F_OUT_PITCH + (lane & 3) * 16);
+              if (r0 + r < left && n < args.nout) *reinterpret_cast<uint4*>(C + (row0 + r0 + r) * args.nout + n) = w;
+            }
+          } else {
+            for (int r = 0; r < 16 && r0 + r < left; ++r)
+              if (n0 + lane < args.nout)
+                C[(row0 + r0 + r) * args.nout + n0 + lane] =
+                    *reinterpret_cast<const bf16*>(stage + r * F_OUT_PITCH + lane * 2);
+          }
+        }
       } else {
         const int unit0 = tl.o * 128 + (int)rank * 64 + quarter * 16;  // hidden units of this warp
         const bool up_first = tl.group == args.shared_group ? args.s_up_first : args.up_first;
         // the activation in place: acc[..][0] holds its pair of rows
         float m[32];
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
+        for (int b = 0; b < 8; ++b)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             float mx = 0.f, my = 0.f;
-            if (b * 32 < cw) {
+            if (b * 16 < cw) {
 #pragma unroll
               for (int l16 = 0; l16 < 2; ++l16) {
                 const float2 p = unpack64(acc[b][l16][j][0]), q = unpack64(acc[b][l16][j][1]);
@@ -786,8 +818,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 acc[b][l16][j][0] = pack64(__float_as_uint(vx), __float_as_uint(vy));
               }
             }
-            m[b * 8 + j * 2] = mx;
-            m[b * 8 + j * 2 + 1] = my;
+            m[b * 4 + j * 2] = mx;
+            m[b * 4 + j * 2 + 1] = my;
           }
         // each row's largest magnitude over the 8 lanes that share its column: a
         // reduce-scatter, after which a lane holds 4 of the 32 rows
@@ -803,7 +835,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int i0 = ((lane & 16) ? 16 : 0) + ((lane & 8) ? 8 : 0) + ((lane & 4) ? 4 : 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = i0 + i;  // b * 8 + j * 2 + e
+          const int at = i0 + i;  // b * 4 + j * 2 + e
           const int c = (at >> 1) * 8 + c_lane + (at & 1);
           if (c < cw) atomicMax(&amax_sh[hf * cw + c], __float_as_uint(m[i]));
         }
@@ -836,15 +868,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int unit = unit0 + (item >> 1) * 8 + (lane >> 4) * 4;
         const int left = min(valid, cw);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (b * 32 >= cw) continue;
+        for (int b = 0; b < 8; ++b) {
+          if (b * 16 >= cw) continue;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 inv = *reinterpret_cast<const float2*>(inv_sh + hf * 128 + b * 32 + (j >> 1) * 16 +
-                                                                (lane & 3) * 4 + (j & 1) * 2);
+          for (int j = 0; j < 2; ++j) {
+            const float2 inv = *reinterpret_cast<const float2*>(inv_sh + hf * 128 + b * 16 + (lane & 3) * 4 + j * 2);
             const float2 lo = unpack64(acc[b][0][j][0]), hi = unpack64(acc[b][1][j][0]);
             const uint32_t w = f8_transpose_bytes(e4m3x4(lo.x * inv.x, lo.y * inv.y, hi.x * inv.x, hi.y * inv.y));
-            const int r = b * 32 + j * 8 + c_lane + (item & 1);
+            const int r = b * 16 + j * 8 + c_lane + (item & 1);
             if (r < left && unit < args.nout) *reinterpret_cast<uint32_t*>(C + (row0 + r) * args.nout + unit) = w;
           }
         }
