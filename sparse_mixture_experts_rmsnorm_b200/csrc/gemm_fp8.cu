@@ -30,7 +30,7 @@
 // between the roles with setmaxnreg):
 //   warp 0      TMA producer in both CTAs; 3-stage ring of 64 KiB, two k-blocks
 //               per stage and (K % 128 == 0) one load per operand and stage;
-//   warp 1      TMEM allocation; in the even CTA lane 0 issues the MMAs;
+//   warp 1      TMEM allocation; in the even CTA it issues the MMAs;
 //   warps 2, 3  scale products, one warp per TMEM slot;
 //   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
 //               of the chunk's columns.
@@ -64,7 +64,7 @@ constexpr int F_RUN = 8;                              // chunks that walk a grou
 constexpr int F_XMAPS = 16;                           // row boxes of 8, 16, ..., 128 rows
 constexpr int F_TRING = 8;
 constexpr int F_SLOTS = 2;                            // rows of scale products, one per TMEM slot
-// readers of a published tile index: even CTA: MMA thread, 2 scale and 8 epilogue
+// readers of a published tile index: even CTA: MMA, 2 scale and 8 epilogue
 // warps; odd CTA: producer, 2 and 8
 constexpr int F_TRING_READERS = 22;
 constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's 16 x 32 bf16 output block
@@ -228,14 +228,24 @@ __device__ __forceinline__ void f8_load_5d(uint32_t dst, const CUtensorMap* map,
 }
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 operands, fp32 accumulation, K = 32.
-__device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+template <int ACCUMULATE>
+__device__ __forceinline__ void f8_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(ACCUMULATE)
       : "memory");
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), A and B
 // e4m3 (bits 7-9 and 10-12 = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
@@ -588,52 +598,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       }
     } else if (warp == 1) {
       // ======================= MMA issuer (even CTA) =======================
-      if (leader && lane == 0) {
-        int stage = 0;
-        uint32_t phase = 0;
-        int buf = 0;
-        uint32_t bphase = 0;
+      // The whole warp runs the loop, so that descriptors and addresses stay in
+      // uniform registers; one elected lane issues.
+      if (leader) {
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, bphase = 0;
         bool ok = true;
-        int rs = 0;
+        int rs = 0, t;
         uint32_t rph = 0;
-        while (ok) {
-          if (!f8_wait<true>(&tr_full[rs], rph, args, &abort_flag, F_SITE_RING)) break;
-          const int t = tile_ring[rs];
-          mbar_arrive(&tr_empty[rs]);
-          if (++rs == F_TRING) {
-            rs = 0;
-            rph ^= 1u;
-          }
-          if (t >= total_tiles) break;
+        const uint64_t desc0 = sw128_desc(smem_base);
+        while (ok && take_warp(rs, rph, t) && t < total_tiles) {
           const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
           const uint32_t idesc = f8_idesc(256, tl.n);
-          const uint32_t x_kblk = (uint32_t)((tl.n >> 1) * F_BK);
-          for (int ks = 0; ks < n_stage_tiles && ok; ++ks) {
-            if (!f8_wait<false>(&full_bar[stage], phase, args, &abort_flag, SITE_FULL)) {
+          const uint32_t x_kblk = (uint32_t)((tl.n >> 1) * F_BK) >> 4;  // in descriptor units of 16 bytes
+          for (int kb = 0; kb < nk; ++kb) {
+            const int j = kb & (F_KB - 1);
+            if (j == 0 && !f8_warp_wait<false>(&full_bar[stage], phase, args, &abort_flag, SITE_FULL)) {
               ok = false;
               break;
             }
-            const uint32_t sa = smem_base + stage * F_STAGE_BYTES;
-            const int kb_n = min(F_KB, nk - ks * F_KB);
-            for (int j = 0; j < kb_n; ++j) {
-              if (!f8_wait<true>(&tempty_bar[buf], bphase ^ 1u, args, &abort_flag, SITE_TMEM_EMPTY)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t d_tmem = tmem_base + (uint32_t)(buf * 256);
-              const uint64_t adesc = sw128_desc(sa + (uint32_t)(j * F_KBLK_BYTES));
-              const uint64_t bdesc = sw128_desc(sa + F_A_BYTES + (uint32_t)j * x_kblk);
-#pragma unroll
-              for (int kk = 0; kk < F_BK / 32; ++kk)  // K = 32 per MMA: 32 bytes further along the row
-                f8_mma(d_tmem, adesc + (uint64_t)(kk * 2), bdesc + (uint64_t)(kk * 2), idesc, kk != 0);
-              tc2_commit_both(&tfull_bar[buf]);
-              buf ^= 1;
-              if (buf == 0) bphase ^= 1u;
+            if (!f8_warp_wait<false>(&tempty_bar[buf], bphase ^ 1u, args, &abort_flag, SITE_TMEM_EMPTY)) {
+              ok = false;
+              break;
             }
-            if (!ok) break;
-            tc2_commit_both(&empty_bar[stage]);
-            if (++stage == F_STAGES) {
+            tc_fence_after();
+            const bool last = j == F_KB - 1 || kb + 1 == nk;  // of its stage
+            if (elect_one()) {
+              const uint64_t adesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + j * (F_KBLK_BYTES >> 4));
+              const uint64_t bdesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + (F_A_BYTES >> 4)) + j * x_kblk;
+              const uint32_t d_tmem = tmem_base + (uint32_t)(buf * 256);
+              f8_mma<0>(d_tmem, adesc, bdesc, idesc);
+#pragma unroll
+              for (int kk = 1; kk < F_BK / 32; ++kk)  // K = 32 per MMA: 32 bytes further along the row
+                f8_mma<1>(d_tmem, adesc + (uint64_t)(kk * 2), bdesc + (uint64_t)(kk * 2), idesc);
+              tc2_commit_both(&tfull_bar[buf]);
+              if (last) tc2_commit_both(&empty_bar[stage]);
+            }
+            __syncwarp();
+            buf ^= 1;
+            if (buf == 0) bphase ^= 1u;
+            if (last && ++stage == F_STAGES) {
               stage = 0;
               phase ^= 1u;
             }
@@ -641,8 +645,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         }
         // Drain: every MMA issued here completes before TMEM is freed and
         // before the odd CTA (whose shared memory they read) may exit.
-        tc2_commit_own(&drain_bar);
-        mbar_wait_bounded(&drain_bar, 0, args.wait_ns, nullptr, args.hdr, KID_GEMM_FP8, SITE_DRAIN);
+        if (elect_one()) {
+          tc2_commit_own(&drain_bar);
+          mbar_wait_bounded(&drain_bar, 0, args.wait_ns, nullptr, args.hdr, KID_GEMM_FP8, SITE_DRAIN);
+        }
+        __syncwarp();
       }
     } else {
       // ======================= scale products (warps 2, 3) =======================
