@@ -5,26 +5,33 @@
 // Epilogues: bf16 or fp32 results, or for the experts' gate and up projections
 //   t = silu(gate) * up  in fp32, quantised per row and 128 hidden units.
 //
-// The operands are swapped as in gemm_swap.cu: 256 weight rows per SM pair on
-// the MMA's M side, a chunk of up to 256 of the group's rows on its N side (a
-// group of m rows is cut into ceil(m / 256) equal chunks, padded to 16 rows).
-//
 // Scales.  They change every 128 columns, so every k-block of 128 gets its own
 // accumulator in one of two 256-column TMEM slots, and eight epilogue warps per
 // CTA add it, times its scales, to fp32 sums in registers: 128 of them per
-// thread, acc += v * (sa * sb) as packed pairs.  A warp reads TMEM in the
-// 16x256b shape (lane l holds rows l / 4 and l / 4 + 8, columns 2 (l % 4) and
-// + 1 of every eight), so one product sa * sb, read from shared memory, serves
-// four values.  Two warps beside the producer and the MMA issuer form those
-// products, their inputs loaded two k-blocks ahead, and complete the same barrier
-// as the accumulator.  A warp loads the next 16 columns, across k-blocks too,
-// before it adds the last ones.
+// thread, acc += v * (sa * sb) as packed pairs.  Two warps beside the producer
+// and the MMA issuer form the products sa * sb, their inputs loaded two k-blocks
+// ahead, and complete the same barrier as the accumulator.  An epilogue warp
+// loads its next 16 columns, across k-blocks too, before it adds the last ones.
 //
-// Gate and up.  One 5-D view over both matrices (their distance is a stride)
-// interleaves them in shared memory, eight gate rows, eight up rows, so a
-// thread holds both values of a hidden unit and the activation needs no
-// exchange.  A pair's tile is 128 hidden units, one block of the result's
-// scales: only each row's largest magnitude crosses between the CTAs.
+// Two tilings (template parameter WIDE):
+//   wide    256 rows of a group on the MMA's M side, 256 weight rows on its N side.
+//           A TMEM lane is a row, so a thread's scale is one number and the
+//           accumulator is read in the fast 32x32b shape.
+//   swapped 256 weight rows on M, a chunk of up to 256 rows, padded to 16, on N (a
+//           group of m rows is cut into ceil(m / 256) equal chunks): no work for
+//           rows that are not there.  A lane is a weight row and the scales differ
+//           by column; in the 16x256b shape (lane l holds rows l / 4 and l / 4 + 8,
+//           columns 2 (l % 4) and + 1 of every eight) one product read from shared
+//           memory serves four values.
+// Measured on B200 with the MMAs running beside it, a 256 x 256 k-block of a pair
+// takes the epilogue about 460 cycles in the 32x32b shape and 980 in the 16x256b
+// shape (which moves half as much per access); the MMAs themselves take 512.
+//
+// Gate and up.  One view over both matrices (their distance is a stride)
+// interleaves them in shared memory, eight gate rows, eight up rows, so a thread
+// holds both values of a hidden unit and the activation needs no exchange.  A
+// pair's tile is 128 hidden units, one block of the result's scales: only each
+// row's largest magnitude crosses between warps (wide) or CTAs (swapped).
 //
 // Roles (384 threads per CTA, clusters of two; the register file is split
 // between the roles with setmaxnreg):
@@ -33,7 +40,7 @@
 //   warp 1      TMEM allocation; in the even CTA it issues the MMAs;
 //   warps 2, 3  scale products, one warp per TMEM slot;
 //   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
-//               of the chunk's columns.
+//               of the tile's columns.
 // Tiles run group by group, a group's chunks in runs of eight per weight tile,
 // and are claimed from a counter in the workspace header that the last pair to
 // finish sets back to zero.  Data that crosses to the other CTA travels by
@@ -55,8 +62,8 @@ constexpr int F_BK = 128;                             // k-block: 128 e4m3 codes
 constexpr int F_KB = 2;                               // k-blocks per stage
 constexpr int F_STAGES = 3;
 constexpr int F_KBLK_BYTES = 128 * F_BK;              // one k-block of 128 rows: 16 KiB
-constexpr int F_A_BYTES = F_KB * F_KBLK_BYTES;        // this CTA's 128 weight rows
-constexpr int F_STAGE_BYTES = 2 * F_A_BYTES;          // and up to 128 rows of the chunk
+constexpr int F_W_BYTES = F_KB * F_KBLK_BYTES;        // this CTA's 128 weight rows
+constexpr int F_STAGE_BYTES = 2 * F_W_BYTES;          // and up to 128 rows of the chunk
 constexpr int F_THREADS = 384;
 constexpr int F_EPI_WARP0 = 4, F_EPI_WARPS = 8;
 constexpr int F_CHUNK = 256;                          // most rows of a group in one tile
@@ -67,18 +74,22 @@ constexpr int F_SLOTS = 2;                            // rows of scale products,
 // readers of a published tile index: even CTA: MMA, 2 scale and 8 epilogue
 // warps; odd CTA: producer, 2 and 8
 constexpr int F_TRING_READERS = 22;
-constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's 16 x 32 bf16 output block
-constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;
+constexpr int F_WIDE_ROWS = 96;                       // rows a group from which on the wide tiling is taken
+constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's output block of 64-byte rows
+constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;         // swapped: 16 rows of 32 bf16
+constexpr int F_OUT_WIDE_BYTES = 32 * F_OUT_PITCH;    // wide: 32 rows
 constexpr int F_CLAIM_WORD = 40, F_DONE_WORD = 41;    // header words: tiles claimed, pairs finished
 
-template <int EPI>
-constexpr int f8_mats() {  // weight matrices per tile
-  return EPI == moe_host::EPI_SWIGLU ? 2 : 1;
+// Rows of scale products per slot of 256 (swapped), and floats of a slot.
+template <int EPI, bool WIDE>
+constexpr int f8_mats() {
+  return EPI == moe_host::EPI_SWIGLU && !WIDE ? 2 : 1;
 }
-template <int EPI>
+template <int EPI, bool WIDE>
 constexpr int f8_smem_bytes() {
-  return F_STAGES * F_STAGE_BYTES + F_SLOTS * f8_mats<EPI>() * F_CHUNK * 4 +
-         (EPI == moe_host::EPI_STORE ? F_EPI_WARPS * F_OUT_BYTES : 0) + 1024;  // + alignment slack
+  return F_STAGES * F_STAGE_BYTES + F_SLOTS * f8_mats<EPI, WIDE>() * F_CHUNK * 4 +
+         (WIDE ? F_EPI_WARPS * F_OUT_WIDE_BYTES : EPI == moe_host::EPI_STORE ? F_EPI_WARPS * F_OUT_BYTES : 0) +
+         1024;  // + alignment slack
 }
 
 struct Fp8Maps {
@@ -100,7 +111,7 @@ struct Fp8Args {
   int up_first, s_up_first;            // SwiGLU: the up matrix comes first in a tile (it lies lower in memory)
   void* c;
   float* c_scale;
-  int vec;                 // 1: 16-byte stores of whole groups of 8 columns
+  int vec;                 // 1: rows of C are whole, aligned 16-byte pieces
   int shared_group, shared_a;
   int32_t* hdr;
   uint64_t wait_ns;
@@ -110,7 +121,7 @@ enum { F_SITE_RING = 8, F_SITE_SCALE = 9, F_SITE_AMAX = 10 };
 
 // ---- tiles --------------------------------------------------------------------
 struct Fp8Tile {
-  int group, row0, rows, n, o;  // rows [row0, row0 + rows) of C; n = rows rounded up to 16; weight tile o
+  int group, row0, rows, half, o;  // rows [row0, row0 + rows) of C; half: rows that each CTA loads; weight tile o
 };
 
 __device__ __forceinline__ int f8_chunks(int m) { return (m + F_CHUNK - 1) / F_CHUNK; }
@@ -134,6 +145,7 @@ __device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int grou
   if (lane == 0) prefix[groups] = carry;
 }
 
+template <bool WIDE>
 __device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, int groups, int n_o) {
   int lo = 0, hi = groups - 1;  // last g with prefix[g] <= t
   while (lo < hi) {
@@ -143,7 +155,7 @@ __device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int
   }
   const int m = offs[lo + 1] - offs[lo];
   const int ch = f8_chunks(m);
-  const int nc = ((m + ch - 1) / ch + 15) & ~15;
+  const int nc = WIDE ? F_CHUNK : ((m + ch - 1) / ch + 15) & ~15;
   const int local = t - prefix[lo];
   const int run = local / (n_o * F_RUN);
   const int rem = local - run * n_o * F_RUN;
@@ -154,7 +166,7 @@ __device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int
   tl.o = rem / in_run;
   tl.row0 = offs[lo] + c * nc;
   tl.rows = max(0, min(nc, m - c * nc));
-  tl.n = max(16, (tl.rows + 15) & ~15);
+  tl.half = WIDE ? min(128, max(8, (tl.rows + 7) & ~7)) : max(8, ((tl.rows + 15) & ~15) >> 1);
   return tl;
 }
 
@@ -164,6 +176,19 @@ __device__ __forceinline__ bool f8_try_wait_cluster(uint64_t* bar, uint32_t pari
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -261,6 +286,16 @@ constexpr uint32_t f8_idesc(int m, int n) {
                  "=r"((r)[7])                                                                                      \
                : "r"(taddr))
 
+// 32 TMEM lanes (lane l = TMEM lane l) x 16 columns.
+#define MOE_TMEM_LD32x16(taddr, r)                                                                                 \
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "   \
+               "%13, %14, %15}, [%16];"                                                                            \
+               : "=r"((r)[0][0]), "=r"((r)[0][1]), "=r"((r)[0][2]), "=r"((r)[0][3]), "=r"((r)[0][4]),              \
+                 "=r"((r)[0][5]), "=r"((r)[0][6]), "=r"((r)[0][7]), "=r"((r)[1][0]), "=r"((r)[1][1]),              \
+                 "=r"((r)[1][2]), "=r"((r)[1][3]), "=r"((r)[1][4]), "=r"((r)[1][5]), "=r"((r)[1][6]),              \
+                 "=r"((r)[1][7])                                                                                   \
+               : "r"(taddr))
+
 // Waits for this thread's TMEM loads; the registers pass through it, so no use of them can move above it.
 __device__ __forceinline__ void f8_tmem_wait(uint32_t (&v)[2][8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -327,26 +362,35 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
     MOE_TMEM_LD16x16(at + (16u << 16), r[1]);
   };
   auto wait_full = [&]() -> bool {
-    if (!f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL)) return false;
-    tc_fence_after();
-    return true;
+    return f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL);
   };
   if (!wait_full()) return false;
+  tc_fence_after();
   load(d.slot, 0, v[0]);
   // one k-block whose first batch is on its way into v[P]
   auto step = [&](auto first, bool more) -> bool {
     constexpr int P = decltype(first)::value;
     const int slot = d.slot;
     const float* sc = d.scales + slot * (MATS * F_CHUNK);
+    ulonglong2 s[2][2];  // scale products of two batches
+    auto scales = [&](int b, ulonglong2 (&q)[2]) {
+      q[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 16);
+      q[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 16) : q[0];
+    };
+    scales(0, s[0]);
+    d.slot ^= 1;
+    if (d.slot == 0) d.phase ^= 1u;
+    bool ready = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint32_t(&r)[2][8] = v[(P + b) & 1];
+      if (b + 1 < NB) scales(b + 1, s[(b + 1) & 1]);
+      // the next k-block is usually there by now: asked before the last batch is awaited
+      if (b + 1 == NB) ready = more && __all_sync(0xffffffffu, mbar_test_wait(d.tfull + d.slot, d.phase));
       f8_tmem_wait(r);
-      if (b + 1 < NB) load(slot, b + 1, v[(P + b + 1) & 1]);
-      ulonglong2 s[2];
-      s[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 16);
-      s[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 16) : s[0];
-      if (b + 1 == NB) {
+      if (b + 1 < NB) {
+        load(slot, b + 1, v[(P + b + 1) & 1]);
+      } else {
         // the slot's accumulator and scale products have been read
         tc_fence_before();
         __syncwarp();
@@ -354,10 +398,9 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
           mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)slot * 8u);
           mbar_arrive(d.sempty + slot);
         }
-        d.slot ^= 1;
-        if (d.slot == 0) d.phase ^= 1u;
         if (more) {
-          if (!wait_full()) return false;
+          if (!ready && !wait_full()) return false;
+          tc_fence_after();
           load(d.slot, 0, v[(P + b + 1) & 1]);
         }
       }
@@ -365,8 +408,9 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
       for (int l16 = 0; l16 < 2; ++l16)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          fma2(acc[b][l16][0][h], pack64(r[l16][2 * h], r[l16][2 * h + 1]), s[h].x);
-          fma2(acc[b][l16][1][h], pack64(r[l16][4 + 2 * h], r[l16][5 + 2 * h]), s[h].y);
+          const ulonglong2 q = s[b & 1][h];
+          fma2(acc[b][l16][0][h], pack64(r[l16][2 * h], r[l16][2 * h + 1]), q.x);
+          fma2(acc[b][l16][1][h], pack64(r[l16][4 + 2 * h], r[l16][5 + 2 * h]), q.y);
         }
     }
     return true;
@@ -378,11 +422,111 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
   return true;
 }
 
-template <int EPI>
+// The wide tiling: acc[16 columns][pairs], lane = row, columns col0 .. + 127.
+// SWIGLU: of every 16 columns the first eight belong to the tile's first matrix.
+template <bool SWIGLU>
+__device__ __forceinline__ bool f8_accumulate_wide(uint64_t (&acc)[8][8], Fp8Drain& d, int col0, int nk,
+                                                   const Fp8Args& args, volatile int* abort) {
+  uint32_t v[2][2][8];
+  auto wait_full = [&]() -> bool {
+    return f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL);
+  };
+  auto load = [&](int slot, int b, uint32_t (&r)[2][8]) {
+    MOE_TMEM_LD32x16(d.tmem + (uint32_t)(slot * 256 + col0 + b * 16), r);
+  };
+  if (!wait_full()) return false;
+  tc_fence_after();
+  load(d.slot, 0, v[0]);
+  for (int kb = 0; kb < nk; ++kb) {
+    const bool more = kb + 1 < nk;
+    const int slot = d.slot;
+    const uint32_t s0 = __float_as_uint(d.scales[slot * F_CHUNK]);
+    const uint32_t s1 = SWIGLU ? __float_as_uint(d.scales[slot * F_CHUNK + 128]) : s0;
+    const uint64_t p0 = pack64(s0, s0), p1 = pack64(s1, s1);
+    d.slot ^= 1;
+    if (d.slot == 0) d.phase ^= 1u;
+    bool ready = false;
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      uint32_t(&r)[2][8] = v[b & 1];
+      // the next k-block is usually there by now: asked before the last batch is awaited
+      if (b == 7) ready = more && __all_sync(0xffffffffu, mbar_test_wait(d.tfull + d.slot, d.phase));
+      f8_tmem_wait(r);
+      if (b < 7) {
+        load(slot, b + 1, v[(b + 1) & 1]);
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane_id() == 0) {
+          mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)slot * 8u);
+          mbar_arrive(d.sempty + slot);
+        }
+        if (more) {
+          if (!ready && !wait_full()) return false;
+          tc_fence_after();
+          load(d.slot, 0, v[0]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        fma2(acc[b][i], pack64(r[0][2 * i], r[0][2 * i + 1]), p0);
+        fma2(acc[b][4 + i], pack64(r[1][2 * i], r[1][2 * i + 1]), p1);
+      }
+    }
+  }
+  return true;
+}
+
+// A warp whose rows are not in the tile: it only hands the slots back.
+__device__ __forceinline__ bool f8_pass_over(Fp8Drain& d, int nk, const Fp8Args& args, volatile int* abort) {
+  for (int kb = 0; kb < nk; ++kb) {
+    if (!f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL)) return false;
+    if (lane_id() == 0) {
+      mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)d.slot * 8u);
+      mbar_arrive(d.sempty + d.slot);
+    }
+    d.slot ^= 1;
+    if (d.slot == 0) d.phase ^= 1u;
+  }
+  return true;
+}
+
+// Writes 64 bytes (w) of each of the warp's 32 rows, lane = row, to C: row r at
+// c + r * ld, `valid` rows, of which the first `bytes` bytes exist.  Through the
+// warp's block of shared memory, so that a store instruction writes whole
+// 64-byte pieces of eight rows.  vec: c, ld and bytes are multiples of 16.
+template <int ES>
+__device__ __forceinline__ void f8_store_rows(uint8_t* stage, const uint4 (&w)[4], uint8_t* c, size_t ld, int valid,
+                                              int bytes, bool vec) {
+  const int lane = lane_id();
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stage + lane * F_OUT_PITCH + i * 16) = w[i];
+  __syncwarp();
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 8 + (lane >> 2), at = (lane & 3) * 16;
+      const uint4 q = *reinterpret_cast<const uint4*>(stage + r * F_OUT_PITCH + at);
+      if (r < valid && at < bytes) *reinterpret_cast<uint4*>(c + (size_t)r * ld + at) = q;
+    }
+  } else {
+    constexpr int COLS = 64 / ES;
+    for (int i = lane; i < 32 * COLS; i += 32) {
+      const int r = i / COLS, at = (i % COLS) * ES;
+      if (r < valid && at < bytes) {
+        if (ES == 4) *reinterpret_cast<float*>(c + (size_t)r * ld + at) = *reinterpret_cast<const float*>(stage + r * F_OUT_PITCH + at);
+        else *reinterpret_cast<bf16*>(c + (size_t)r * ld + at) = *reinterpret_cast<const bf16*>(stage + r * F_OUT_PITCH + at);
+      }
+    }
+  }
+}
+
+template <int EPI, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args args) {
   constexpr bool SWIGLU = EPI == moe_host::EPI_SWIGLU;
-  constexpr int MATS = f8_mats<EPI>();
+  constexpr int MATS = f8_mats<EPI, WIDE>();
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[F_STAGES];   // used in the even CTA
   __shared__ __align__(8) uint64_t empty_bar[F_STAGES];
@@ -400,9 +544,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   __shared__ volatile int abort_flag;
   __shared__ int offs_sh[TC_MAX_GROUPS + 1];
   __shared__ int prefix_sh[TC_MAX_GROUPS + 1];
-  __shared__ unsigned amax_sh[SWIGLU ? F_CHUNK : 1];
-  __shared__ volatile float peer_sh[SWIGLU ? 2 : 1][SWIGLU ? F_CHUNK : 1];
-  __shared__ __align__(16) float inv_sh[SWIGLU ? F_CHUNK : 4];
+  __shared__ unsigned amax_sh[SWIGLU && !WIDE ? F_CHUNK : 1];
+  __shared__ volatile float peer_sh[SWIGLU && !WIDE ? 2 : 1][SWIGLU && !WIDE ? F_CHUNK : 1];
+  __shared__ __align__(16) float inv_sh[SWIGLU && !WIDE ? F_CHUNK : 4];
+  __shared__ __align__(8) uint64_t half_bar[4];          // SwiGLU, wide: both halves of a quarter's rows are in half_sh
+  __shared__ float half_sh[SWIGLU && WIDE ? 2 : 1][2][128];
 
   const int warp = warp_id(), lane = lane_id();
   const uint32_t rank = cluster_rank();
@@ -415,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   const int G = args.groups;
   for (int i = threadIdx.x; i <= G; i += blockDim.x)
     offs_sh[i] = args.offsets ? args.offsets[i] : (i == 0 ? 0 : args.max_rows);
-  if constexpr (SWIGLU)
+  if constexpr (SWIGLU && !WIDE)
     for (int i = threadIdx.x; i < F_CHUNK; i += blockDim.x) amax_sh[i] = 0u;
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
@@ -433,6 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     }
     mbar_init(&amax_bar, F_EPI_WARPS);
     mbar_init(&inv_bar, F_EPI_WARPS);
+    for (int q = 0; q < 4; ++q) mbar_init(&half_bar[q], 2);
     for (int j = 0; j < F_TRING; ++j) {
       mbar_init(&tr_full[j], 1);
       mbar_init(&tr_empty[j], F_TRING_READERS);
@@ -518,16 +665,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           ok = take(t);
         }
         while (ok && t < total_tiles) {
-          const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
           const bool sh = tl.group == args.shared_group;
           const CUtensorMap* wm = sh ? &maps.ws : &maps.w;
           const bool own_rows = sh && args.shared_a;
-          const int half = tl.n >> 1;  // rows of the chunk in each CTA (8 .. 128)
-          const CUtensorMap* xm = own_rows ? &maps.xs[half / 8 - 1] : &maps.x[half / 8 - 1];
-          const int x_row = (own_rows ? tl.row0 - offs_sh[tl.group] : tl.row0) + (int)rank * half;
+          const CUtensorMap* xm = own_rows ? &maps.xs[tl.half / 8 - 1] : &maps.x[tl.half / 8 - 1];
+          const int x_row = (own_rows ? tl.row0 - offs_sh[tl.group] : tl.row0) + (int)rank * (WIDE ? 128 : tl.half);
           const int w_base = sh ? 0 : tl.group * args.nout;
           const int w_row = SWIGLU ? (w_base + tl.o * 128 + (int)rank * 64) / 8 : w_base + tl.o * 256 + (int)rank * 128;
-          const uint32_t x_kblk = (uint32_t)(half * F_BK);
+          const uint32_t x_kblk = (uint32_t)(tl.half * F_BK);
           int next = 0;
           bool sent = !leader;
           for (int ks = 0; ks < n_stage_tiles; ++ks) {
@@ -543,13 +689,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             if (args.view) {
               if (SWIGLU) f8_load_5d(sa, wm, full_leader, w_row, ks * F_KB);
               else f8_load_3d(sa, wm, full_leader, 0, w_row, ks * F_KB);
-              f8_load_3d(sa + F_A_BYTES, xm, full_leader, 0, x_row, ks * F_KB);
+              f8_load_3d(sa + F_W_BYTES, xm, full_leader, 0, x_row, ks * F_KB);
             } else {
               for (int j = 0; j < kb_n; ++j) {
                 const int c0 = (ks * F_KB + j) * F_BK;
                 if (SWIGLU) f8_load_4d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
                 else f8_load_2d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
-                f8_load_2d(sa + F_A_BYTES + j * x_kblk, xm, full_leader, c0, x_row);
+                f8_load_2d(sa + F_W_BYTES + j * x_kblk, xm, full_leader, c0, x_row);
               }
             }
             ++issued;
@@ -608,9 +754,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         uint32_t rph = 0;
         const uint64_t desc0 = sw128_desc(smem_base);
         while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-          const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
-          const uint32_t idesc = f8_idesc(256, tl.n);
-          const uint32_t x_kblk = (uint32_t)((tl.n >> 1) * F_BK) >> 4;  // in descriptor units of 16 bytes
+          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+          const uint32_t idesc = f8_idesc(256, WIDE ? 256 : 2 * tl.half);
+          const uint32_t x_kblk = (uint32_t)(tl.half * F_BK) >> 4;  // in descriptor units of 16 bytes
           for (int kb = 0; kb < nk; ++kb) {
             const int j = kb & (F_KB - 1);
             if (j == 0 && !f8_warp_wait<false>(&full_bar[stage], phase, args, &abort_flag, SITE_FULL)) {
@@ -624,8 +770,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             tc_fence_after();
             const bool last = j == F_KB - 1 || kb + 1 == nk;  // of its stage
             if (elect_one()) {
-              const uint64_t adesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + j * (F_KBLK_BYTES >> 4));
-              const uint64_t bdesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + (F_A_BYTES >> 4)) + j * x_kblk;
+              const uint64_t wdesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + j * (F_KBLK_BYTES >> 4));
+              const uint64_t xdesc = desc0 + (uint64_t)(stage * (F_STAGE_BYTES >> 4) + (F_W_BYTES >> 4)) + j * x_kblk;
+              const uint64_t adesc = WIDE ? xdesc : wdesc, bdesc = WIDE ? wdesc : xdesc;
               const uint32_t d_tmem = tmem_base + (uint32_t)(buf * 256);
               f8_mma<0>(d_tmem, adesc, bdesc, idesc);
 #pragma unroll
@@ -660,30 +807,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       const int nkb = nk;
       bool ok = true;
       while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-        const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
+        const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
         const bool sh = tl.group == args.shared_group;
         const bool own_rows = sh && args.shared_a;
         const float* as = own_rows ? args.sas + (size_t)(tl.row0 - offs_sh[tl.group]) * nkb
                                    : args.as + (size_t)tl.row0 * nkb;
-        const int nb = SWIGLU ? tl.o : min(2 * tl.o + (int)rank, args.nnb - 1);
-        const size_t b_at = ((size_t)(sh ? 0 : tl.group) * args.nnb + nb) * nkb;
-        const float* b0 = (sh ? args.sbs[0] : args.bs[0]) + b_at;
-        const float* b1 = (sh ? args.sbs[MATS - 1] : args.bs[MATS - 1]) + b_at;
-        const int cw = tl.n >> 1;
-        float cur[8], cur_b[2];
-        auto load = [&](int kb, float (&v)[8], float (&b)[2]) {
+        // the two weight scales of a k-block: of the tile's two matrices (SwiGLU), or of
+        // the two halves of its columns (wide); else this CTA's only one
+        const float* bs0 = (sh ? args.sbs[0] : args.bs[0]) + (size_t)(sh ? 0 : tl.group) * args.nnb * nkb;
+        const float* bs1 = (sh ? args.sbs[1] : args.bs[1]) + (size_t)(sh ? 0 : tl.group) * args.nnb * nkb;
+        const float* b0 = bs0 + (size_t)(SWIGLU ? tl.o : min(2 * tl.o + (WIDE ? 0 : (int)rank), args.nnb - 1)) * nkb;
+        const float* b1 = SWIGLU ? bs1 + (size_t)tl.o * nkb : bs0 + (size_t)min(2 * tl.o + 1, args.nnb - 1) * nkb;
+        const int r_base = WIDE ? (int)rank * 128 : 0;  // first row whose products this CTA needs
+        constexpr int RP = WIDE ? 4 : 8;                // rows per lane
+        float cur[RP], cur_b[2];
+        auto load = [&](int kb, float (&v)[RP], float (&b)[2]) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = lane + 32 * i;
+          for (int i = 0; i < RP; ++i) {
+            const int r = r_base + lane + 32 * i;
             v[i] = r < tl.rows ? __ldg(as + (size_t)r * nkb + kb) : 0.f;
           }
           b[0] = __ldg(b0 + kb);
-          b[1] = MATS == 2 ? __ldg(b1 + kb) : 0.f;
+          b[1] = SWIGLU || WIDE ? __ldg(b1 + kb) : 0.f;
         };
         const int kb0 = (int)((kc ^ (uint32_t)warp) & 1u);  // this warp's first k-block of the tile
         if (kb0 < nk) load(kb0, cur, cur_b);
         for (int kb = kb0; kb < nk; kb += 2) {
-          float nxt[8], nxt_b[2];
+          float nxt[RP], nxt_b[2];
           if (kb + 2 < nk) load(kb + 2, nxt, nxt_b);
           if (!f8_warp_wait<false>(&sempty_bar[slot], sphase ^ 1u, args, &abort_flag, F_SITE_SCALE)) {
             ok = false;
@@ -692,10 +842,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           sphase ^= 1u;
           float* dst = scale_ring + slot * (MATS * F_CHUNK);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < RP; ++i) {
             const int r = lane + 32 * i;
-            if (r < tl.n) {
-              const int at = r < cw ? f8_scale_at(r) : 128 + f8_scale_at(r - cw);
+            if constexpr (WIDE) {
+              dst[r] = __fmul_rn(cur[i], cur_b[0]);
+              dst[128 + r] = __fmul_rn(cur[i], cur_b[1]);
+            } else if (r < 2 * tl.half) {
+              const int at = r < tl.half ? f8_scale_at(r) : 128 + f8_scale_at(r - tl.half);
 #pragma unroll
               for (int m = 0; m < MATS; ++m) dst[m * F_CHUNK + at] = __fmul_rn(cur[i], cur_b[m]);
             }
@@ -703,7 +856,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&tfull_bar[slot]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
+          for (int i = 0; i < RP; ++i) cur[i] = nxt[i];
           cur_b[0] = nxt_b[0];
           cur_b[1] = nxt_b[1];
         }
@@ -722,16 +875,102 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     drain.tempty_remote = map_to_rank(&tempty_bar[0], 0);
     drain.tfull = tfull_bar;
     drain.sempty = sempty_bar;
-    drain.scales = scale_ring + hf * 128 + (lane & 3) * 4;
+    drain.scales = scale_ring + (WIDE ? (SWIGLU ? 0 : hf * 128) + quarter * 32 + lane : hf * 128 + (lane & 3) * 4);
     drain.phase = 0;
     drain.slot = 0;
-    uint32_t tiles_done = 0;
+    uint32_t tiles_done = 0, half_phase = 0;
     int rs = 0, t;
     uint32_t rph = 0;
     bool ok = true;
     while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-      const Fp8Tile tl = f8_decode(t, prefix_sh, offs_sh, G, args.n_o);
-      const int cw = tl.n >> 1;  // columns of this warp: hf * cw .. + cw - 1
+      const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+      if constexpr (WIDE) {
+        const int r_cta = quarter * 32;                          // this warp's rows of the CTA's 128
+        const int valid = tl.rows - ((int)rank * 128 + r_cta);   // ... of which this many exist
+        if (valid <= 0) {
+          ok = f8_pass_over(drain, nk, args, &abort_flag);
+          if (!ok) break;
+          if constexpr (SWIGLU) ++tiles_done;  // both warps of the quarter pass the tile over
+          continue;
+        }
+        uint64_t acc[8][8];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i >> 3][i & 7] = 0ull;
+        ok = f8_accumulate_wide<SWIGLU>(acc, drain, hf * 128, nk, args, &abort_flag);
+        if (!ok) break;
+        uint8_t* stage = smem + F_STAGES * F_STAGE_BYTES + F_SLOTS * MATS * F_CHUNK * 4 +
+                         (warp - F_EPI_WARP0) * F_OUT_WIDE_BYTES;
+        const size_t row = (size_t)tl.row0 + (int)rank * 128 + r_cta;
+        if constexpr (!SWIGLU) {
+          constexpr int ES = EPI == moe_host::EPI_F32 ? 4 : 2, COLS = 64 / ES;
+          const int n0 = tl.o * 256 + hf * 128;
+          const size_t ld = (size_t)args.nout * ES;
+          uint8_t* c = reinterpret_cast<uint8_t*>(args.c) + row * ld + (size_t)n0 * ES;
+#pragma unroll
+          for (int p = 0; p < 128 / COLS; ++p) {  // 16 (fp32) or 32 columns per pass
+            const int left = args.nout - (n0 + p * COLS);
+            if (left <= 0) break;
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (ES == 4) {
+                const float2 x = unpack64(acc[p][2 * i]), y = unpack64(acc[p][2 * i + 1]);
+                w[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                                  __float_as_uint(y.y));
+              } else {
+                const uint64_t* a = &acc[2 * p + (i >> 1)][(i & 1) * 4];
+                const float2 x = unpack64(a[0]), y = unpack64(a[1]), z = unpack64(a[2]), q = unpack64(a[3]);
+                w[i] = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y), pack_bf16x2(z.x, z.y),
+                                  pack_bf16x2(q.x, q.y));
+              }
+            }
+            f8_store_rows<ES>(stage, w, c + p * 64, ld, valid, left * ES, args.vec);
+          }
+        } else {
+          const bool up_first = tl.group == args.shared_group ? args.s_up_first : args.up_first;
+          const int unit0 = tl.o * 128 + hf * 64;  // this warp's hidden units, 8 per 16 columns
+          float m = 0.f;
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = unpack64(acc[b][i]), y = unpack64(acc[b][4 + i]);
+              const bool in = unit0 + b * 8 + 2 * i < args.nout;  // nout is even
+              const float v0 = in ? __fmul_rn(f8_silu(up_first ? y.x : x.x), up_first ? x.x : y.x) : 0.f;
+              const float v1 = in ? __fmul_rn(f8_silu(up_first ? y.y : x.y), up_first ? x.y : y.y) : 0.f;
+              m = fmaxf(m, fmaxf(fabsf(v0), fabsf(v1)));
+              acc[b][i] = pack64(__float_as_uint(v0), __float_as_uint(v1));
+            }
+          // the other half of the row's 128 units is with the warp of the same rows.
+          // Two buffers: that warp reads this tile's value before it arrives for the next.
+          float* at = &half_sh[tiles_done & 1u][0][r_cta + lane];
+          at[hf * 128] = m;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&half_bar[quarter]);
+          if (!f8_warp_wait<false>(&half_bar[quarter], half_phase, args, &abort_flag, F_SITE_AMAX)) break;
+          half_phase ^= 1u;
+          ++tiles_done;
+          const float scale = quant_scale(fmaxf(m, at[(hf ^ 1) * 128]));
+          const float inv = __frcp_rn(scale);
+          if (hf == 0 && lane < valid) args.c_scale[(row + lane) * args.n_o + tl.o] = scale;
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t* a = &acc[2 * i + (k >> 1)][(k & 1) * 2];
+              const float2 x = unpack64(a[0]), y = unpack64(a[1]);
+              q[k] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+            }
+            w[i] = make_uint4(q[0], q[1], q[2], q[3]);
+          }
+          if (unit0 < args.nout)
+            f8_store_rows<1>(stage, w, reinterpret_cast<uint8_t*>(args.c) + row * args.nout + unit0, args.nout, valid,
+                             args.nout - unit0, true);
+        }
+      } else {
+      const int cw = tl.half;  // columns of this warp: hf * cw .. + cw - 1
       uint64_t acc[8][2][2][2];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i >> 3][(i >> 2) & 1][(i >> 1) & 1][i & 1] = 0ull;
@@ -852,15 +1091,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const uint32_t pb = tiles_done & 1u, pph = (tiles_done >> 1) & 1u;
         if (!f8_warp_wait<false>(&amax_bar, once, args, &abort_flag, F_SITE_AMAX)) break;
         // one thread per row: trade the magnitude with the other CTA, make the scale
-        if (owner == 0) mbar_arrive_expect_tx(&peer_bar[pb], (uint32_t)tl.n * 4u);
+        if (owner == 0) mbar_arrive_expect_tx(&peer_bar[pb], (uint32_t)(2 * tl.half) * 4u);
         unsigned mine = 0u;
-        if (owner < tl.n) {
+        if (owner < 2 * tl.half) {
           mine = amax_sh[owner];
           amax_sh[owner] = 0u;
           st_async_b32(map_to_rank((const void*)&peer_sh[pb][owner], peer), mine, map_to_rank(&peer_bar[pb], peer));
         }
         if (!f8_warp_wait<true>(&peer_bar[pb], pph, args, &abort_flag, F_SITE_AMAX)) break;
-        if (owner < tl.n) {
+        if (owner < 2 * tl.half) {
           const float scale = quant_scale(fmaxf(__uint_as_float(mine), peer_sh[pb][owner]));
           inv_sh[owner < cw ? f8_scale_at(owner) : 128 + f8_scale_at(owner - cw)] = __frcp_rn(scale);
           if (leader && owner < tl.rows) args.c_scale[(size_t)(tl.row0 + owner) * args.n_o + tl.o] = scale;
@@ -886,6 +1125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             if (r < left && unit < args.nout) *reinterpret_cast<uint32_t*>(C + (row0 + r) * args.nout + unit) = w;
           }
         }
+      }
       }
     }
   }
@@ -946,7 +1186,7 @@ static bool interleaved_map(CUtensorMap* m, const void* low, int64_t apart, int6
 }
 
 // Clusters of two that can be resident at once (one CTA per SM), per device.
-template <int EPI>
+template <int EPI, bool WIDE>
 static int f8_resident_pairs() {
   static std::atomic<int> cache[64] = {};
   const int dev = current_device();
@@ -958,8 +1198,8 @@ static int f8_resident_pairs() {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
   cfg.blockDim = dim3(moe::F_THREADS);
-  cfg.dynamicSmemBytes = moe::f8_smem_bytes<EPI>();
-  if (cudaOccupancyMaxActiveClusters(&n, moe::gemm_fp8_kernel<EPI>, &cfg) != cudaSuccess || n <= 0) {
+  cfg.dynamicSmemBytes = moe::f8_smem_bytes<EPI, WIDE>();
+  if (cudaOccupancyMaxActiveClusters(&n, moe::gemm_fp8_kernel<EPI, WIDE>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = sm_count() / 2;
   }
@@ -968,17 +1208,23 @@ static int f8_resident_pairs() {
   return n;
 }
 
-template <int EPI>
+template <int EPI, bool WIDE>
 static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound, cudaStream_t s) {
   static SmemLimit lim;
-  const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI>, moe::f8_smem_bytes<EPI>(), lim);
+  const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI, WIDE>, moe::f8_smem_bytes<EPI, WIDE>(), lim);
   if (st != MOE_OK) return st;
-  const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI>());
-  moe::gemm_fp8_kernel<EPI><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI>(), s>>>(maps, args);
+  const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI, WIDE>());
+  moe::gemm_fp8_kernel<EPI, WIDE><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI, WIDE>(), s>>>(maps, args);
   return launch_status();
 }
 
-// Weight map(s) of one set of matrices; *up_first: the second lies lower in memory.
+template <int EPI>
+static moe_status launch_f8(bool wide, const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound,
+                            cudaStream_t s) {
+  return wide ? launch_f8_t<EPI, true>(maps, args, tile_bound, s) : launch_f8_t<EPI, false>(maps, args, tile_bound, s);
+}
+
+// Weight map of one set of matrices; *up_first: the second lies lower in memory.
 static moe_status weight_map(CUtensorMap* m, int epi, const Fp8Operand& b, const Fp8Operand& b2, int64_t rows, int k,
                              bool view, int* up_first) {
   *up_first = 0;
@@ -994,6 +1240,7 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.max_rows == 0) return MOE_OK;
   const bool swiglu = g.epi == EPI_SWIGLU;
   const bool view = g.k % 128 == 0;
+  const bool wide = (int64_t)g.max_rows >= (int64_t)moe::F_WIDE_ROWS * (g.offsets ? g.groups : 1);
   const bool shared = g.sb.q != nullptr && g.offsets != nullptr;
   const bool shared_a = shared && g.sa.q != nullptr && g.sa_rows > 0;
   moe::Fp8Maps maps;
@@ -1009,13 +1256,13 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   // row boxes: only those that a chunk can take (one group: its two chunk sizes)
   auto row_maps = [&](CUtensorMap* ms, const Fp8Operand& a, int64_t rows, bool one_group) -> bool {
     const int64_t ch = (rows + moe::F_CHUNK - 1) / moe::F_CHUNK;
-    const int64_t nc = ((rows + ch - 1) / ch + 15) / 16 * 16;
-    const int64_t last = std::max<int64_t>(16, (rows - (ch - 1) * nc + 15) / 16 * 16);
-    const int64_t most = std::min<int64_t>(moe::F_CHUNK, (rows + 15) / 16 * 16);
+    const int64_t nc = wide ? moe::F_CHUNK : ((rows + ch - 1) / ch + 15) / 16 * 16;
+    auto half = [&](int64_t r) { return wide ? std::min<int64_t>(128, (r + 7) / 8 * 8) : (r + 15) / 16 * 8; };
+    const int64_t first = half(std::min(nc, rows)), last = half(rows - (ch - 1) * nc);
     for (int i = 0; i < moe::F_XMAPS; ++i) {
-      const int64_t n = 16 * (i + 1);
-      if (one_group ? (n == nc || n == last) : n <= most)
-        if (!rows_map(&ms[i], a.q, rows, g.k, a.ld, 8 * (i + 1), view)) return false;
+      const int64_t box = 8 * (i + 1);
+      if (one_group ? (box == first || box == last) : box <= half(std::min<int64_t>(moe::F_CHUNK, rows)))
+        if (!rows_map(&ms[i], a.q, rows, g.k, a.ld, (int)box, view)) return false;
     }
     return true;
   };
@@ -1038,7 +1285,7 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   }
   args.c = g.c;
   args.c_scale = g.c_scale;
-  args.vec = (g.nout % 8 == 0 && (uintptr_t)g.c % 16 == 0) ? 1 : 0;
+  args.vec = (g.nout % (g.epi == EPI_F32 ? 4 : 8) == 0 && (uintptr_t)g.c % 16 == 0) ? 1 : 0;
   args.shared_group = shared ? g.groups - 1 : -1;
   args.shared_a = shared_a ? 1 : 0;
   args.hdr = g.hdr;
@@ -1046,9 +1293,9 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   // upper bound on the tiles; the exact count lives on the device
   const int64_t chunks = (int64_t)(g.max_rows + moe::F_CHUNK - 1) / moe::F_CHUNK + (g.offsets ? args.groups : 0);
   const int64_t bound = chunks * args.n_o;
-  if (swiglu) return launch_f8_t<EPI_SWIGLU>(maps, args, bound, s);
-  if (g.epi == EPI_F32) return launch_f8_t<EPI_F32>(maps, args, bound, s);
-  return launch_f8_t<EPI_STORE>(maps, args, bound, s);
+  if (swiglu) return launch_f8<EPI_SWIGLU>(wide, maps, args, bound, s);
+  if (g.epi == EPI_F32) return launch_f8<EPI_F32>(wide, maps, args, bound, s);
+  return launch_f8<EPI_STORE>(wide, maps, args, bound, s);
 }
 
 }  // namespace moe_host
