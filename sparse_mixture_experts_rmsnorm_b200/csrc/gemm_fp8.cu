@@ -183,19 +183,6 @@ __device__ __forceinline__ bool f8_try_wait_cluster(uint64_t* bar, uint32_t pari
   return ok != 0;
 }
 
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // One thread's bounded wait; CLUSTER: a barrier that the other CTA arrives on.
 template <bool CLUSTER>
 __device__ __forceinline__ bool f8_wait(uint64_t* bar, uint32_t parity, const Fp8Args& a, volatile int* abort,
@@ -339,15 +326,59 @@ __device__ __forceinline__ uint32_t f8_transpose_bytes(uint32_t w) {
   return b0 ? __byte_perm(w, p, 0x3715) : __byte_perm(w, p, 0x6240);
 }
 
-// What the main loop of an epilogue warp needs, set up once.
+// What the main loop of an epilogue warp needs, set up once; barriers and scales as shared-memory addresses.
 struct Fp8Drain {
   uint32_t tmem;            // this warp's lanes of slot 0
   uint32_t tempty_remote;   // the even CTA's tempty_bar[0]
-  uint64_t *tfull, *sempty; // this CTA's barriers of slot 0
-  const float* scales;      // this lane's first scale product of slot 0
-  uint32_t phase;           // of the next k-block's tfull
-  int slot;                 // ... and its slot
+  uint32_t tfull, sempty;   // this CTA's barriers of slot 0
+  uint32_t scales;          // this lane's first scale product of slot 0
+  uint32_t slot, phase;     // slot of the next k-block, and its tfull's phase
 };
+
+__device__ __forceinline__ uint32_t ld_shared(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void ld_shared_2x64(uint32_t at, uint64_t (&v)[2]) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0]), "=l"(v[1]) : "r"(at) : "memory");
+}
+
+// Whether the phase has completed, for every lane; without waiting.
+__device__ __forceinline__ bool f8_ready(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
+}
+
+__device__ __forceinline__ bool f8_wait_at(uint32_t bar, uint32_t phase, const Fp8Args& args, volatile int* abort,
+                                           int site) {
+  if (__builtin_expect(f8_ready(bar, phase), 1)) return true;
+  return f8_warp_wait<false>(reinterpret_cast<uint64_t*>(__cvta_shared_to_generic(bar)), phase, args, abort, site);
+}
+
+// Waits for the accumulator and the scale products of the next k-block.
+__device__ __forceinline__ bool f8_next_full(const Fp8Drain& d, const Fp8Args& args, volatile int* abort) {
+  if (!f8_wait_at(d.tfull + d.slot * 8u, d.phase, args, abort, SITE_TMEM_FULL)) return false;
+  tc_fence_after();
+  return true;
+}
+
+// Hands the slot back: its accumulator and scale products have been read.
+__device__ __forceinline__ void f8_release(const Fp8Drain& d, uint32_t slot) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane_id() == 0) {
+    mbar_arrive_cluster_relaxed(d.tempty_remote + slot * 8u);
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(d.sempty + slot * 8u) : "memory");
+  }
+}
 
 // Adds the k-blocks of one tile to acc[16 columns][16 lanes][8 columns][rows
 // l / 4, + 8] (pairs of columns).  NB batches of 16 columns from column col0 of
@@ -356,50 +387,40 @@ template <int NB, int MATS>
 __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Drain& d, int col0, int nk,
                                               const Fp8Args& args, volatile int* abort) {
   uint32_t v[2][2][8];
-  auto load = [&](int slot, int b, uint32_t (&r)[2][8]) {
-    const uint32_t at = d.tmem + (uint32_t)(slot * 256 + col0 + b * 16);
+  auto load = [&](uint32_t slot, int b, uint32_t (&r)[2][8]) {
+    const uint32_t at = d.tmem + slot * 256u + (uint32_t)(col0 + b * 16);
     MOE_TMEM_LD16x16(at, r[0]);
     MOE_TMEM_LD16x16(at + (16u << 16), r[1]);
   };
-  auto wait_full = [&]() -> bool {
-    return f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL);
-  };
-  if (!wait_full()) return false;
-  tc_fence_after();
+  if (!f8_next_full(d, args, abort)) return false;
   load(d.slot, 0, v[0]);
   // one k-block whose first batch is on its way into v[P]
   auto step = [&](auto first, bool more) -> bool {
     constexpr int P = decltype(first)::value;
-    const int slot = d.slot;
-    const float* sc = d.scales + slot * (MATS * F_CHUNK);
-    ulonglong2 s[2][2];  // scale products of two batches
-    auto scales = [&](int b, ulonglong2 (&q)[2]) {
-      q[0] = *reinterpret_cast<const ulonglong2*>(sc + b * 16);
-      q[1] = MATS == 2 ? *reinterpret_cast<const ulonglong2*>(sc + F_CHUNK + b * 16) : q[0];
+    const uint32_t slot = d.slot;
+    const uint32_t sc = d.scales + slot * (MATS * F_CHUNK * 4);
+    uint64_t s[2][2][2];  // scale products of two batches
+    auto scales = [&](int b) {
+      ld_shared_2x64(sc + b * 64, s[b & 1][0]);
+      if (MATS == 2) ld_shared_2x64(sc + F_CHUNK * 4 + b * 64, s[b & 1][1]);
     };
-    scales(0, s[0]);
-    d.slot ^= 1;
-    if (d.slot == 0) d.phase ^= 1u;
+    scales(0);
+    d.slot ^= 1u;
+    d.phase ^= d.slot ^ 1u;
     bool ready = false;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint32_t(&r)[2][8] = v[(P + b) & 1];
-      if (b + 1 < NB) scales(b + 1, s[(b + 1) & 1]);
+      if (b + 1 < NB) scales(b + 1);
       // the next k-block is usually there by now: asked before the last batch is awaited
-      if (b + 1 == NB) ready = more && __all_sync(0xffffffffu, mbar_test_wait(d.tfull + d.slot, d.phase));
+      if (b + 1 == NB) ready = more && f8_ready(d.tfull + d.slot * 8u, d.phase);
       f8_tmem_wait(r);
       if (b + 1 < NB) {
         load(slot, b + 1, v[(P + b + 1) & 1]);
       } else {
-        // the slot's accumulator and scale products have been read
-        tc_fence_before();
-        __syncwarp();
-        if (lane_id() == 0) {
-          mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)slot * 8u);
-          mbar_arrive(d.sempty + slot);
-        }
+        f8_release(d, slot);
         if (more) {
-          if (!ready && !wait_full()) return false;
+          if (!ready && !f8_next_full(d, args, abort)) return false;
           tc_fence_after();
           load(d.slot, 0, v[(P + b + 1) & 1]);
         }
@@ -408,9 +429,9 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
       for (int l16 = 0; l16 < 2; ++l16)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const ulonglong2 q = s[b & 1][h];
-          fma2(acc[b][l16][0][h], pack64(r[l16][2 * h], r[l16][2 * h + 1]), q.x);
-          fma2(acc[b][l16][1][h], pack64(r[l16][4 + 2 * h], r[l16][5 + 2 * h]), q.y);
+          const uint64_t* q = s[b & 1][MATS == 2 ? h : 0];
+          fma2(acc[b][l16][0][h], pack64(r[l16][2 * h], r[l16][2 * h + 1]), q[0]);
+          fma2(acc[b][l16][1][h], pack64(r[l16][4 + 2 * h], r[l16][5 + 2 * h]), q[1]);
         }
     }
     return true;
@@ -423,70 +444,62 @@ __device__ __forceinline__ bool f8_accumulate(uint64_t (&acc)[8][2][2][2], Fp8Dr
 }
 
 // The wide tiling: acc[16 columns][pairs], lane = row, columns col0 .. + 127.
+// (Single FMAs: packed ones measured 3 % slower here.)
 // SWIGLU: of every 16 columns the first eight belong to the tile's first matrix.
 template <bool SWIGLU>
 __device__ __forceinline__ bool f8_accumulate_wide(uint64_t (&acc)[8][8], Fp8Drain& d, int col0, int nk,
                                                    const Fp8Args& args, volatile int* abort) {
   uint32_t v[2][2][8];
-  auto wait_full = [&]() -> bool {
-    return f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL);
+  auto load = [&](uint32_t slot, int b, uint32_t (&r)[2][8]) {
+    MOE_TMEM_LD32x16(d.tmem + slot * 256u + (uint32_t)(col0 + b * 16), r);
   };
-  auto load = [&](int slot, int b, uint32_t (&r)[2][8]) {
-    MOE_TMEM_LD32x16(d.tmem + (uint32_t)(slot * 256 + col0 + b * 16), r);
-  };
-  if (!wait_full()) return false;
-  tc_fence_after();
+  if (!f8_next_full(d, args, abort)) return false;
   load(d.slot, 0, v[0]);
-  for (int kb = 0; kb < nk; ++kb) {
-    const bool more = kb + 1 < nk;
-    const int slot = d.slot;
-    const uint32_t s0 = __float_as_uint(d.scales[slot * F_CHUNK]);
-    const uint32_t s1 = SWIGLU ? __float_as_uint(d.scales[slot * F_CHUNK + 128]) : s0;
-    const uint64_t p0 = pack64(s0, s0), p1 = pack64(s1, s1);
-    d.slot ^= 1;
-    if (d.slot == 0) d.phase ^= 1u;
-    bool ready = false;
+  auto step = [&](auto last) -> bool {
+    constexpr bool MORE = decltype(last)::value;
+    const uint32_t slot = d.slot;
+    const float s0 = __uint_as_float(ld_shared(d.scales + slot * (F_CHUNK * 4)));
+    const float s1 = SWIGLU ? __uint_as_float(ld_shared(d.scales + slot * (F_CHUNK * 4) + 512)) : s0;
+    d.slot ^= 1u;
+    d.phase ^= d.slot ^ 1u;
 #pragma unroll
     for (int b = 0; b < 8; ++b) {
       uint32_t(&r)[2][8] = v[b & 1];
-      // the next k-block is usually there by now: asked before the last batch is awaited
-      if (b == 7) ready = more && __all_sync(0xffffffffu, mbar_test_wait(d.tfull + d.slot, d.phase));
       f8_tmem_wait(r);
       if (b < 7) {
         load(slot, b + 1, v[(b + 1) & 1]);
       } else {
-        tc_fence_before();
-        __syncwarp();
-        if (lane_id() == 0) {
-          mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)slot * 8u);
-          mbar_arrive(d.sempty + slot);
-        }
-        if (more) {
-          if (!ready && !wait_full()) return false;
-          tc_fence_after();
+        f8_release(d, slot);
+        if (MORE) {
+          if (!f8_next_full(d, args, abort)) return false;
           load(d.slot, 0, v[0]);
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        fma2(acc[b][i], pack64(r[0][2 * i], r[0][2 * i + 1]), p0);
-        fma2(acc[b][4 + i], pack64(r[1][2 * i], r[1][2 * i + 1]), p1);
+        float2 x = unpack64(acc[b][i]), y = unpack64(acc[b][4 + i]);
+        x.x = __fmaf_rn(__uint_as_float(r[0][2 * i]), s0, x.x);
+        x.y = __fmaf_rn(__uint_as_float(r[0][2 * i + 1]), s0, x.y);
+        y.x = __fmaf_rn(__uint_as_float(r[1][2 * i]), s1, y.x);
+        y.y = __fmaf_rn(__uint_as_float(r[1][2 * i + 1]), s1, y.y);
+        acc[b][i] = pack64(__float_as_uint(x.x), __float_as_uint(x.y));
+        acc[b][4 + i] = pack64(__float_as_uint(y.x), __float_as_uint(y.y));
       }
     }
-  }
-  return true;
+    return true;
+  };
+  for (int kb = 1; kb < nk; ++kb)
+    if (!step(std::true_type())) return false;
+  return step(std::false_type());
 }
 
 // A warp whose rows are not in the tile: it only hands the slots back.
 __device__ __forceinline__ bool f8_pass_over(Fp8Drain& d, int nk, const Fp8Args& args, volatile int* abort) {
   for (int kb = 0; kb < nk; ++kb) {
-    if (!f8_warp_wait<false>(d.tfull + d.slot, d.phase, args, abort, SITE_TMEM_FULL)) return false;
-    if (lane_id() == 0) {
-      mbar_arrive_cluster_relaxed(d.tempty_remote + (uint32_t)d.slot * 8u);
-      mbar_arrive(d.sempty + d.slot);
-    }
-    d.slot ^= 1;
-    if (d.slot == 0) d.phase ^= 1u;
+    if (!f8_next_full(d, args, abort)) return false;
+    f8_release(d, d.slot);
+    d.slot ^= 1u;
+    d.phase ^= d.slot ^ 1u;
   }
   return true;
 }
@@ -873,11 +886,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     Fp8Drain drain;
     drain.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16);
     drain.tempty_remote = map_to_rank(&tempty_bar[0], 0);
-    drain.tfull = tfull_bar;
-    drain.sempty = sempty_bar;
-    drain.scales = scale_ring + (WIDE ? (SWIGLU ? 0 : hf * 128) + quarter * 32 + lane : hf * 128 + (lane & 3) * 4);
-    drain.phase = 0;
-    drain.slot = 0;
+    drain.tfull = smem_u32(tfull_bar);
+    drain.sempty = smem_u32(sempty_bar);
+    drain.scales = smem_u32(scale_ring) +
+                   4u * (uint32_t)(WIDE ? (SWIGLU ? 0 : hf * 128) + quarter * 32 + lane : hf * 128 + (lane & 3) * 4);
+    drain.slot = drain.phase = 0;
     uint32_t tiles_done = 0, half_phase = 0;
     int rs = 0, t;
     uint32_t rph = 0;
