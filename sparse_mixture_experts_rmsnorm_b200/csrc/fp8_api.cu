@@ -1,6 +1,7 @@
 // C-ABI entry points of the 8-bit (e4m3, block-scaled) operators and of the
 // layer forward built on them: argument checks, the workspace layout and the
 // order of the kernels on the caller's stream.
+#include <algorithm>
 #include <initializer_list>
 
 #include "gemm_fp8_kernels.h"
@@ -14,11 +15,12 @@ namespace moe_host {
 // their scales, the e4m3 activations with theirs, and the expert outputs.
 struct Fp8Layout {
   size_t hdr, xn, xq, xs, logits, idx, gate, counts, offsets, offsets_ext, slot_row, row_token, hist, xq_perm,
-      xs_perm, act, act_s, y_perm, y_shared, total;
+      xs_perm, act, act_s, y_perm, y_shared, split, total;
   bool fold;           // the shared expert runs as one more group of the routed products
   int64_t rows;        // R: rows of the expert-sorted buffers
   int64_t act_elems;   // codes and scales that the activation regions hold
   int64_t act_scales;
+  size_t split_bytes;  // partial sums of products with few tiles
 };
 
 static Fp8Layout fp8_layout(const moe_config* c) {
@@ -41,7 +43,7 @@ static Fp8Layout fp8_layout(const moe_config* c) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  L.hdr = take(moe::kHeaderBytes);
+  L.hdr = take(kFp8HeaderBytes);
   L.xn = take(N * d * es);
   L.xq = take(N * d);
   L.xs = take(N * q_blocks(c->d_model) * 4);
@@ -60,6 +62,17 @@ static Fp8Layout fp8_layout(const moe_config* c) {
   L.act_s = take(L.act_scales * 4);
   L.y_perm = take(Rx * d * es);
   L.y_shared = take(c->d_ff_shared > 0 && !L.fold ? N * d * es : 0);
+  // both products of the routed experts, of one group of as many rows and of the shared expert
+  L.split_bytes = 0;
+  auto need = [&](int64_t rows, int groups, bool offs, int64_t h) {
+    const size_t gate_up = gemm_fp8_split_bytes(true, rows, groups, offs, (int)h, c->d_model);
+    const size_t down = gemm_fp8_split_bytes(false, rows, groups, offs, c->d_model, (int)h);
+    L.split_bytes = std::max(L.split_bytes, std::max(gate_up, down));
+  };
+  need(Rx, (int)E + (L.fold ? 1 : 0), true, c->d_ff);
+  need(Rx, 1, false, c->d_ff);
+  if (c->d_ff_shared > 0) need(N, 1, false, c->d_ff_shared);
+  L.split = take(L.split_bytes);
   L.total = o;
   return L;
 }
@@ -101,6 +114,8 @@ static moe_status ffn_fp8_impl(const moe_config* c, Fp8Gemm p, Fp8Operand w_down
   act.scale = (float*)wsp(ws, L.act_s);
   act.ld = d_ff;
   p.hdr = (int32_t*)wsp(ws, L.hdr);
+  p.split_ws = wsp(ws, L.split);
+  p.split_bytes = L.split_bytes;
   p.epi = EPI_SWIGLU;
   p.nout = d_ff;
   p.k = c->d_model;
@@ -158,7 +173,8 @@ moe_status moe_quantize_fp8(int32_t dtype, int32_t block_rows, int32_t n_mats, i
 
 size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n_out, int32_t k) {
   if (n_groups < 1 || n_groups > moe::TC_MAX_GROUPS || max_rows < 0 || n_out < 1 || k < 1) return 0;
-  return moe::kHeaderBytes;
+  return kFp8HeaderBytes + std::max(gemm_fp8_split_bytes(false, max_rows, n_groups, true, n_out, k),
+                                    gemm_fp8_split_bytes(false, max_rows, n_groups, false, n_out, k));
 }
 
 moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_rows, int32_t n_out, int32_t k,
@@ -184,6 +200,8 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
   g.k = k;
   g.c = c;
   g.hdr = (int32_t*)ws;
+  g.split_ws = wsp(ws, kFp8HeaderBytes);
+  g.split_bytes = ws_bytes - kFp8HeaderBytes;
   return launch_gemm_fp8(g, (cudaStream_t)stream);
 }
 

@@ -41,6 +41,9 @@
 //   warps 2, 3  scale products, one warp per TMEM slot;
 //   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
 //               of the tile's columns.
+// Few tiles (a handful of rows): each is cut along K into `splits` parts, so that
+// the weights stream through all SMs; the parts' fp32 sums meet in the workspace
+// and the CTA that comes last adds them in order and writes the result.
 // Tiles run group by group, a group's chunks in runs of eight per weight tile,
 // and are claimed from a counter in the workspace header that the last pair to
 // finish sets back to zero.  Data that crosses to the other CTA travels by
@@ -103,6 +106,10 @@ struct Fp8Args {
   int groups, max_rows;
   int nout;                // output columns per group
   int nk;                  // k-blocks
+  int splits;              // parts that a tile's k-blocks are cut into
+  unsigned* split_count;   // [tiles] parts done
+  float4* partial;         // [tiles][splits][2][partial_vecs][256]
+  int partial_vecs;        // float4 per thread and part
   int n_o;                 // weight tiles per group
   int view;                // 1: the maps bring two k-blocks per load (K % 128 == 0)
   int nnb;                 // scale blocks along n
@@ -117,11 +124,13 @@ struct Fp8Args {
   uint64_t wait_ns;
 };
 
-enum { F_SITE_RING = 8, F_SITE_SCALE = 9, F_SITE_AMAX = 10 };
+enum { F_SITE_RING = 8, F_SITE_SCALE = 9, F_SITE_AMAX = 10, F_SITE_SPLIT = 11 };
 
 // ---- tiles --------------------------------------------------------------------
 struct Fp8Tile {
   int group, row0, rows, half, o;  // rows [row0, row0 + rows) of C; half: rows that each CTA loads; weight tile o
+  int kb0, nk;                     // k-blocks kb0 .. kb0 + nk - 1
+  int index, part;                 // of the tile, its parts together; which of them
 };
 
 __device__ __forceinline__ int f8_chunks(int m) { return (m + F_CHUNK - 1) / F_CHUNK; }
@@ -146,7 +155,13 @@ __device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int grou
 }
 
 template <bool WIDE>
-__device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, int groups, int n_o) {
+__device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, int groups, int n_o, int nk,
+                                             int splits) {
+  int part = 0;
+  if (splits > 1) {
+    part = t % splits;
+    t /= splits;
+  }
   int lo = 0, hi = groups - 1;  // last g with prefix[g] <= t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -162,6 +177,10 @@ __device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int
   const int in_run = min(F_RUN, ch - run * F_RUN);
   const int c = run * F_RUN + rem % in_run;
   Fp8Tile tl;
+  tl.index = t;
+  tl.part = part;
+  tl.kb0 = splits > 1 ? nk * part / splits : 0;
+  tl.nk = splits > 1 ? nk * (part + 1) / splits - tl.kb0 : nk;
   tl.group = lo;
   tl.o = rem / in_run;
   tl.row0 = offs[lo] + c * nc;
@@ -535,7 +554,8 @@ __device__ __forceinline__ void f8_store_rows(uint8_t* stage, const uint4 (&w)[4
   }
 }
 
-template <int EPI, bool WIDE>
+// SPLIT: tiles are cut along K into args.splits parts.
+template <int EPI, bool WIDE, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args args) {
   constexpr bool SWIGLU = EPI == moe_host::EPI_SWIGLU;
@@ -549,6 +569,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   __shared__ __align__(8) uint64_t amax_bar;             // SwiGLU: every warp's magnitudes are in amax_sh
   __shared__ __align__(8) uint64_t peer_bar[2];          //         the other CTA's have arrived
   __shared__ __align__(8) uint64_t inv_bar;              //         1 / scale of every row is in inv_sh
+  __shared__ __align__(8) uint64_t split_bar;            // every warp's part of a cut tile is in the workspace
+  __shared__ __align__(8) uint64_t pair_bar;             // ... the odd CTA's too (even CTA)
+  __shared__ __align__(8) uint64_t done_bar;             // last_sh is there
+  __shared__ volatile int last_sh;
   __shared__ __align__(8) uint64_t drain_bar;
   __shared__ __align__(8) uint64_t tr_full[F_TRING];     // a tile index is in tile_ring[j] (both CTAs)
   __shared__ __align__(8) uint64_t tr_empty[F_TRING];    // every reader has taken it (even CTA)
@@ -592,6 +616,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     }
     mbar_init(&amax_bar, F_EPI_WARPS);
     mbar_init(&inv_bar, F_EPI_WARPS);
+    mbar_init(&split_bar, F_EPI_WARPS);
+    mbar_init(&pair_bar, 1);
+    mbar_init(&done_bar, 1);
     for (int q = 0; q < 4; ++q) mbar_init(&half_bar[q], 2);
     for (int j = 0; j < F_TRING; ++j) {
       mbar_init(&tr_full[j], 1);
@@ -612,9 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   cluster_sync();  // both CTAs' barriers are initialised before either signals the other
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_sh;
-  const int total_tiles = prefix_sh[G];
-  const int nk = args.nk;
-  const int n_stage_tiles = (nk + F_KB - 1) / F_KB;  // stages per tile
+  const int total_tiles = prefix_sh[G] * (SPLIT ? args.splits : 1);
 
   // the next published tile index, for a role of one warp (every lane calls) or one thread
   auto take_warp = [&](int& rs, uint32_t& rph, int& t) -> bool {
@@ -678,7 +703,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           ok = take(t);
         }
         while (ok && t < total_tiles) {
-          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
           const bool sh = tl.group == args.shared_group;
           const CUtensorMap* wm = sh ? &maps.ws : &maps.w;
           const bool own_rows = sh && args.shared_a;
@@ -689,7 +714,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           const uint32_t x_kblk = (uint32_t)(tl.half * F_BK);
           int next = 0;
           bool sent = !leader;
-          for (int ks = 0; ks < n_stage_tiles; ++ks) {
+          const int kb_end = tl.kb0 + tl.nk;
+          for (int kb = tl.kb0; kb < kb_end; kb += F_KB) {
             if (!f8_wait<false>(&empty_bar[stage], phase ^ 1u, args, &abort_flag, SITE_EMPTY)) {
               ok = false;
               break;
@@ -697,15 +723,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             const uint32_t sa = smem_base + stage * F_STAGE_BYTES;
             const uint32_t full_leader = map_to_rank(&full_bar[stage], 0);
             // a view load brings F_KB k-blocks (zeros past K), else one load per k-block
-            const int kb_n = args.view ? F_KB : min(F_KB, nk - ks * F_KB);
+            const int kb_n = args.view ? F_KB : min(F_KB, kb_end - kb);
             if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2u * (uint32_t)kb_n * (F_KBLK_BYTES + x_kblk));
             if (args.view) {
-              if (SWIGLU) f8_load_5d(sa, wm, full_leader, w_row, ks * F_KB);
-              else f8_load_3d(sa, wm, full_leader, 0, w_row, ks * F_KB);
-              f8_load_3d(sa + F_W_BYTES, xm, full_leader, 0, x_row, ks * F_KB);
+              if (SWIGLU) f8_load_5d(sa, wm, full_leader, w_row, kb);
+              else f8_load_3d(sa, wm, full_leader, 0, w_row, kb);
+              f8_load_3d(sa + F_W_BYTES, xm, full_leader, 0, x_row, kb);
             } else {
               for (int j = 0; j < kb_n; ++j) {
-                const int c0 = (ks * F_KB + j) * F_BK;
+                const int c0 = (kb + j) * F_BK;
                 if (SWIGLU) f8_load_4d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
                 else f8_load_2d(sa + j * F_KBLK_BYTES, wm, full_leader, c0, w_row);
                 f8_load_2d(sa + F_W_BYTES + j * x_kblk, xm, full_leader, c0, x_row);
@@ -767,9 +793,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         uint32_t rph = 0;
         const uint64_t desc0 = sw128_desc(smem_base);
         while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
           const uint32_t idesc = f8_idesc(256, WIDE ? 256 : 2 * tl.half);
           const uint32_t x_kblk = (uint32_t)(tl.half * F_BK) >> 4;  // in descriptor units of 16 bytes
+          const int nk = tl.nk;
           for (int kb = 0; kb < nk; ++kb) {
             const int j = kb & (F_KB - 1);
             if (j == 0 && !f8_warp_wait<false>(&full_bar[stage], phase, args, &abort_flag, SITE_FULL)) {
@@ -817,20 +844,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       uint32_t rph = 0;
       const int slot = warp & 1;
       uint32_t kc = 0, sphase = 0;  // k-blocks of all tiles so far: k-block kc is in TMEM slot kc % 2
-      const int nkb = nk;
+      const int nkb = args.nk;
       bool ok = true;
       while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-        const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+        const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
         const bool sh = tl.group == args.shared_group;
         const bool own_rows = sh && args.shared_a;
+        const int nk = tl.nk;
         const float* as = own_rows ? args.sas + (size_t)(tl.row0 - offs_sh[tl.group]) * nkb
                                    : args.as + (size_t)tl.row0 * nkb;
+        as += tl.kb0;
         // the two weight scales of a k-block: of the tile's two matrices (SwiGLU), or of
         // the two halves of its columns (wide); else this CTA's only one
         const float* bs0 = (sh ? args.sbs[0] : args.bs[0]) + (size_t)(sh ? 0 : tl.group) * args.nnb * nkb;
         const float* bs1 = (sh ? args.sbs[1] : args.bs[1]) + (size_t)(sh ? 0 : tl.group) * args.nnb * nkb;
-        const float* b0 = bs0 + (size_t)(SWIGLU ? tl.o : min(2 * tl.o + (WIDE ? 0 : (int)rank), args.nnb - 1)) * nkb;
-        const float* b1 = SWIGLU ? bs1 + (size_t)tl.o * nkb : bs0 + (size_t)min(2 * tl.o + 1, args.nnb - 1) * nkb;
+        const float* b0 = bs0 + (size_t)(SWIGLU ? tl.o : min(2 * tl.o + (WIDE ? 0 : (int)rank), args.nnb - 1)) * nkb + tl.kb0;
+        const float* b1 =
+            (SWIGLU ? bs1 + (size_t)tl.o * nkb : bs0 + (size_t)min(2 * tl.o + 1, args.nnb - 1) * nkb) + tl.kb0;
         const int r_base = WIDE ? (int)rank * 128 : 0;  // first row whose products this CTA needs
         constexpr int RP = WIDE ? 4 : 8;                // rows per lane
         float cur[RP], cur_b[2];
@@ -895,22 +925,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     int rs = 0, t;
     uint32_t rph = 0;
     bool ok = true;
+    // Tiles cut along K: this warp's sums go to the workspace (`vecs` float4 per
+    // thread).  Once both CTAs of the pair have written theirs, the even CTA counts
+    // the pair's part as done.  Returns 2, with the sums of all parts in `a`, in the
+    // pair whose part was the last one, 1 in the others, 0 after a failed wait.
+    uint32_t split_phase = 0;
+    auto split_join = [&](uint64_t(&a)[64], const Fp8Tile& tl, int vecs) -> int {
+      const size_t stride = (size_t)args.partial_vecs * 256;  // of one CTA's part
+      float4* const first = args.partial + ((size_t)tl.index * args.splits * 2 + rank) * stride + owner;
+      float4* const mine = first + (size_t)tl.part * 2 * stride;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (i >= vecs) break;
+        const float2 x = unpack64(a[2 * i]), y = unpack64(a[2 * i + 1]);
+        __stcg(mine + i * 256, make_float4(x.x, x.y, y.x, y.y));
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&split_bar);
+      const uint32_t ph = split_phase;
+      split_phase ^= 1u;
+      if (warp == F_EPI_WARP0) {
+        if (!f8_warp_wait<false>(&split_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
+        if (leader) {
+          if (!f8_warp_wait<true>(&pair_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
+          if (lane == 0) {
+            __threadfence();
+            const bool last = atomicInc(args.split_count + tl.index, (unsigned)args.splits - 1u) ==
+                              (unsigned)args.splits - 1u;  // and back to zero for the next launch
+            last_sh = last;
+            mbar_arrive(&done_bar);
+            const uint32_t peer_done = map_to_rank(&done_bar, 1);
+            mbar_arrive_expect_tx_cluster(peer_done, 4);
+            st_async_b32(map_to_rank((const void*)&last_sh, 1), last, peer_done);
+          }
+        } else if (lane == 0) {
+          __threadfence();
+          mbar_arrive_cluster(map_to_rank(&pair_bar, 0));
+        }
+        __syncwarp();
+      }
+      if (!f8_warp_wait<true>(&done_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
+      if (!last_sh) return 1;
+      __threadfence();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) a[i] = 0ull;
+#pragma unroll
+      for (int i0 = 0; i0 < 32; i0 += 4) {
+        if (i0 >= vecs) break;
+        const float4* src = first + i0 * 256;
+#pragma unroll 4  // 16 loads in flight
+        for (int p = 0; p < args.splits; ++p, src += 2 * stride) {
+#pragma unroll
+          for (int i = i0; i < i0 + 4; ++i) {
+            const float4 f = __ldcg(src + (i - i0) * 256);
+            const float2 x = unpack64(a[2 * i]), y = unpack64(a[2 * i + 1]);
+            a[2 * i] = pack64(__float_as_uint(__fadd_rn(x.x, f.x)), __float_as_uint(__fadd_rn(x.y, f.y)));
+            a[2 * i + 1] = pack64(__float_as_uint(__fadd_rn(y.x, f.z)), __float_as_uint(__fadd_rn(y.y, f.w)));
+          }
+        }
+      }
+      return 2;
+    };
     while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-      const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o);
+      const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
       if constexpr (WIDE) {
         const int r_cta = quarter * 32;                          // this warp's rows of the CTA's 128
         const int valid = tl.rows - ((int)rank * 128 + r_cta);   // ... of which this many exist
         if (valid <= 0) {
-          ok = f8_pass_over(drain, nk, args, &abort_flag);
+          ok = f8_pass_over(drain, tl.nk, args, &abort_flag);
           if (!ok) break;
+          if constexpr (SPLIT) {
+            uint64_t none[64] = {};
+            if (split_join(none, tl, 0) == 0) break;
+          }
           if constexpr (SWIGLU) ++tiles_done;  // both warps of the quarter pass the tile over
           continue;
         }
         uint64_t acc[8][8];
 #pragma unroll
         for (int i = 0; i < 64; ++i) acc[i >> 3][i & 7] = 0ull;
-        ok = f8_accumulate_wide<SWIGLU>(acc, drain, hf * 128, nk, args, &abort_flag);
+        ok = f8_accumulate_wide<SWIGLU>(acc, drain, hf * 128, tl.nk, args, &abort_flag);
         if (!ok) break;
+        if constexpr (SPLIT) {
+          const int done = split_join(reinterpret_cast<uint64_t(&)[64]>(acc), tl, 32);
+          if (done == 0) break;
+          if (done == 1) continue;
+        }
         uint8_t* stage = smem + F_STAGES * F_STAGE_BYTES + F_SLOTS * MATS * F_CHUNK * 4 +
                          (warp - F_EPI_WARP0) * F_OUT_WIDE_BYTES;
         const size_t row = (size_t)tl.row0 + (int)rank * 128 + r_cta;
@@ -988,12 +1089,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i >> 3][(i >> 2) & 1][(i >> 1) & 1][i & 1] = 0ull;
       // columns past cw in the last batches add up unused values
-      if (cw > 96) ok = f8_accumulate<8, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
-      else if (cw > 64) ok = f8_accumulate<6, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
-      else if (cw > 32) ok = f8_accumulate<4, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
-      else if (cw > 16) ok = f8_accumulate<2, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
-      else ok = f8_accumulate<1, MATS>(acc, drain, hf * cw, nk, args, &abort_flag);
+      if (cw > 96) ok = f8_accumulate<8, MATS>(acc, drain, hf * cw, tl.nk, args, &abort_flag);
+      else if (cw > 64) ok = f8_accumulate<6, MATS>(acc, drain, hf * cw, tl.nk, args, &abort_flag);
+      else if (cw > 32) ok = f8_accumulate<4, MATS>(acc, drain, hf * cw, tl.nk, args, &abort_flag);
+      else if (cw > 16) ok = f8_accumulate<2, MATS>(acc, drain, hf * cw, tl.nk, args, &abort_flag);
+      else ok = f8_accumulate<1, MATS>(acc, drain, hf * cw, tl.nk, args, &abort_flag);
       if (!ok) break;
+      if constexpr (SPLIT) {
+        const int done = split_join(reinterpret_cast<uint64_t(&)[64]>(acc), tl, (cw + 15) / 16 * 4);
+        if (done == 0) break;
+        if (done == 1) continue;
+      }
 
       const int c_lane = 2 * (lane & 3);  // this lane's first column of every eight
       const int valid = tl.rows - hf * cw;  // rows of this half that exist
@@ -1199,7 +1305,7 @@ static bool interleaved_map(CUtensorMap* m, const void* low, int64_t apart, int6
 }
 
 // Clusters of two that can be resident at once (one CTA per SM), per device.
-template <int EPI, bool WIDE>
+template <int EPI, bool WIDE, bool SPLIT>
 static int f8_resident_pairs() {
   static std::atomic<int> cache[64] = {};
   const int dev = current_device();
@@ -1212,7 +1318,7 @@ static int f8_resident_pairs() {
   cfg.gridDim = dim3((unsigned)(sm_count() & ~1));
   cfg.blockDim = dim3(moe::F_THREADS);
   cfg.dynamicSmemBytes = moe::f8_smem_bytes<EPI, WIDE>();
-  if (cudaOccupancyMaxActiveClusters(&n, moe::gemm_fp8_kernel<EPI, WIDE>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, moe::gemm_fp8_kernel<EPI, WIDE, SPLIT>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = sm_count() / 2;
   }
@@ -1221,20 +1327,24 @@ static int f8_resident_pairs() {
   return n;
 }
 
-template <int EPI, bool WIDE>
+template <int EPI, bool WIDE, bool SPLIT>
 static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound, cudaStream_t s) {
   static SmemLimit lim;
-  const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI, WIDE>, moe::f8_smem_bytes<EPI, WIDE>(), lim);
+  const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI, WIDE, SPLIT>, moe::f8_smem_bytes<EPI, WIDE>(), lim);
   if (st != MOE_OK) return st;
-  const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI, WIDE>());
-  moe::gemm_fp8_kernel<EPI, WIDE><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI, WIDE>(), s>>>(maps, args);
+  const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI, WIDE, SPLIT>());
+  moe::gemm_fp8_kernel<EPI, WIDE, SPLIT><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI, WIDE>(), s>>>(maps, args);
   return launch_status();
 }
 
 template <int EPI>
 static moe_status launch_f8(bool wide, const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound,
                             cudaStream_t s) {
-  return wide ? launch_f8_t<EPI, true>(maps, args, tile_bound, s) : launch_f8_t<EPI, false>(maps, args, tile_bound, s);
+  if (args.splits > 1)
+    return wide ? launch_f8_t<EPI, true, true>(maps, args, tile_bound, s)
+                : launch_f8_t<EPI, false, true>(maps, args, tile_bound, s);
+  return wide ? launch_f8_t<EPI, true, false>(maps, args, tile_bound, s)
+              : launch_f8_t<EPI, false, false>(maps, args, tile_bound, s);
 }
 
 // Weight map of one set of matrices; *up_first: the second lies lower in memory.
@@ -1249,11 +1359,48 @@ static moe_status weight_map(CUtensorMap* m, int epi, const Fp8Operand& b, const
   return interleaved_map(m, low, apart, rows, k, view) ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Wide tiles or swapped ones, weight tiles per group, and the most tiles there can be.
+struct Fp8Shape {
+  bool wide;
+  int n_o;
+  int64_t tiles;
+};
+static Fp8Shape f8_shape(bool swiglu, int64_t rows, int groups, bool offsets, int nout) {
+  Fp8Shape f;
+  f.wide = rows >= (int64_t)moe::F_WIDE_ROWS * groups;
+  f.n_o = swiglu ? (nout + 127) / 128 : (nout + 255) / 256;
+  f.tiles = ((rows + moe::F_CHUNK - 1) / moe::F_CHUNK + (offsets ? groups : 0)) * f.n_o;
+  return f;
+}
+
+// Parts that each tile is cut into along K when there are at most half as many
+// tiles as SM pairs: as many as keep every pair at work, but at least eight
+// k-blocks each (joining the parts costs about as much as those).
+static int f8_splits(const Fp8Shape& f, int nk) {
+  const int64_t pairs = sm_count() / 2;
+  if (f.tiles < 1 || f.tiles > pairs / 2) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(pairs / f.tiles, nk / 8));
+}
+
+// float4 of sums per thread: 128 columns (wide), or half of the chunk in 16s
+static int f8_partial_vecs(const Fp8Shape& f, int64_t rows) {
+  return f.wide ? 32 : (int)((std::min<int64_t>(moe::F_CHUNK, rows) + 31) / 32 * 4);
+}
+
+size_t gemm_fp8_split_bytes(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k) {
+  if (rows <= 0) return 0;
+  const Fp8Shape f = f8_shape(swiglu, rows, groups, offsets, nout);
+  const int splits = f8_splits(f, q_blocks(k));
+  return splits == 1 ? 0 : (size_t)f.tiles * splits * 2 * f8_partial_vecs(f, rows) * 256 * sizeof(float4);
+}
+
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.max_rows == 0) return MOE_OK;
   const bool swiglu = g.epi == EPI_SWIGLU;
+  const int groups = g.offsets ? g.groups : 1;
+  const Fp8Shape shape = f8_shape(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout);
+  const bool wide = shape.wide;
   const bool view = g.k % 128 == 0;
-  const bool wide = (int64_t)g.max_rows >= (int64_t)moe::F_WIDE_ROWS * (g.offsets ? g.groups : 1);
   const bool shared = g.sb.q != nullptr && g.offsets != nullptr;
   const bool shared_a = shared && g.sa.q != nullptr && g.sa_rows > 0;
   moe::Fp8Maps maps;
@@ -1283,11 +1430,21 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (!row_maps(maps.x, g.a, a_rows, g.offsets == nullptr)) return MOE_ERR_CUDA;
   if (shared_a && !row_maps(maps.xs, g.sa, g.sa_rows, true)) return MOE_ERR_CUDA;
   args.offsets = g.offsets;
-  args.groups = g.offsets ? g.groups : 1;
+  args.groups = groups;
   args.max_rows = g.max_rows;
   args.nout = g.nout;
   args.nk = q_blocks(g.k);
-  args.n_o = swiglu ? (g.nout + 127) / 128 : (g.nout + 255) / 256;
+  args.n_o = shape.n_o;
+  args.splits = 1;
+  args.split_count = nullptr;
+  args.partial = nullptr;
+  args.partial_vecs = f8_partial_vecs(shape, g.max_rows);
+  const size_t split_bytes = gemm_fp8_split_bytes(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout, g.k);
+  if (split_bytes > 0 && split_bytes <= g.split_bytes) {
+    args.splits = f8_splits(shape, args.nk);
+    args.split_count = reinterpret_cast<unsigned*>(g.hdr) + moe::kHeaderBytes / 4;
+    args.partial = static_cast<float4*>(g.split_ws);
+  }
   args.view = view ? 1 : 0;
   args.nnb = q_blocks(g.nout);
   args.as = g.a.scale;
@@ -1303,9 +1460,7 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   args.shared_a = shared_a ? 1 : 0;
   args.hdr = g.hdr;
   args.wait_ns = wait_limit_ns();
-  // upper bound on the tiles; the exact count lives on the device
-  const int64_t chunks = (int64_t)(g.max_rows + moe::F_CHUNK - 1) / moe::F_CHUNK + (g.offsets ? args.groups : 0);
-  const int64_t bound = chunks * args.n_o;
+  const int64_t bound = shape.tiles * args.splits;  // the exact count lives on the device
   if (swiglu) return launch_f8<EPI_SWIGLU>(wide, maps, args, bound, s);
   if (g.epi == EPI_F32) return launch_f8<EPI_F32>(wide, maps, args, bound, s);
   return launch_f8<EPI_STORE>(wide, maps, args, bound, s);

@@ -30,8 +30,18 @@ struct Fp8Gemm {
   int groups = 1, max_rows = 0, nout = 0, k = 0;
   void* c = nullptr;         // [max_rows][nout]
   float* c_scale = nullptr;  // EPI_SWIGLU: [max_rows][ceil(nout / 128)]
-  int32_t* hdr = nullptr;
+  int32_t* hdr = nullptr;    // workspace header and, behind it, the counters of cut tiles (kFp8HeaderBytes)
+  void* split_ws = nullptr;  // partial sums of cut tiles
+  size_t split_bytes = 0;
 };
+
+// Start of every workspace of the 8-bit products: the header and the counters of
+// tiles cut along K, all zeroed by moe_workspace_init.
+constexpr size_t kFp8HeaderBytes = 1024;
+
+// Bytes of partial sums for these sizes (0: no tile is cut).  A launch with fewer
+// bytes does not cut its tiles.
+size_t gemm_fp8_split_bytes(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k);
 
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s);
 

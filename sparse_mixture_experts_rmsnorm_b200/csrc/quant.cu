@@ -7,6 +7,8 @@
 //   s  = act(x + residual),  r = fl32(1 / sqrt(mean(s^2) + eps)), mean in fp64,
 //   v  = fl32(fl32(s * r) * w),  xn = act(v),  (q, q_scale) from v per 128 columns.
 // xn has the bits that moe_route gives for h = s.
+#include <algorithm>
+
 #include "gemm_fp8_kernels.h"
 #include "quant_common.cuh"
 
@@ -59,65 +61,85 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
-// One block per row (grid-stride); the row s is staged in shared memory in its
-// own type.  Every warp takes whole blocks of 128 columns in the second pass,
-// so a scale needs no shared memory.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) add_rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ w,
-                                                          T* res_out, T* xn, uint8_t* __restrict__ q,
-                                                          float* __restrict__ q_scale, int n, int d, float eps) {
-  extern __shared__ __align__(16) uint8_t row_raw[];
-  T* row = reinterpret_cast<T*>(row_raw);
-  __shared__ double part[8];
+// One block per row (grid-stride), the row in registers: LANES lanes hold NBW
+// blocks of 128 columns, UNITS apart, so that every sum and every block's largest
+// magnitude is a few shuffles away.  Bound by HBM: each input is read once, each
+// output written once.  With few rows NBW is 1 and the row is spread over up to
+// 1024 threads (latency); else NBW = 4, so that a thread has 8 loads in flight.
+template <typename T, int V, int NBW>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ w,
+                                                           T* res_out, T* xn, uint8_t* __restrict__ q,
+                                                           float* __restrict__ q_scale, int n, int d, float eps) {
+  __shared__ double part[32];
   __shared__ float r_sh;
   constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses;
   const int warps = blockDim.x >> 5;
   const int nb = (d + Q_BLOCK - 1) / Q_BLOCK;
+  const int unit0 = threadIdx.x / LANES, units = blockDim.x / LANES;
+  const int c0 = (threadIdx.x % LANES) * V;
   for (int t = blockIdx.x; t < n; t += gridDim.x) {
     const size_t base = (size_t)t * d;
+    constexpr bool EARLY = NBW == 1;  // few rows: the norm weights are loaded before the sums are joined
+    Pack<T, V> s[NBW][PASSES], wv[EARLY ? PASSES : 1];
+#pragma unroll
+    for (int i = 0; i < NBW; ++i)
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int c = (unit0 + i * units) * Q_BLOCK + p * (LANES * V) + c0;
+        if (c < d) {
+          s[i][p] = load_pack<T, V>(x + base + c);
+          if (residual != nullptr) {
+            const Pack<T, V> b = load_pack<T, V>(residual + base + c);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[i][p].v[j] = from_f32<T>(__fadd_rn(to_f32(s[i][p].v[j]), to_f32(b.v[j])));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) s[i][p].v[j] = from_f32<T>(0.f);
+        }
+      }
     double acc = 0.0;
-    for (int i = threadIdx.x * V; i < d; i += blockDim.x * V) {
-      Pack<T, V> s = load_pack<T, V>(x + base + i);
-      if (residual != nullptr) {
-        const Pack<T, V> b = load_pack<T, V>(residual + base + i);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s.v[j] = from_f32<T>(__fadd_rn(to_f32(s.v[j]), to_f32(b.v[j])));
-      }
-      if (res_out != nullptr) store_pack<T, V>(res_out + base + i, s);
-      store_pack<T, V>(row + i, s);
+    for (int i = 0; i < NBW; ++i)
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const double f = (double)to_f32(s.v[j]);
-        acc += f * f;
+      for (int p = 0; p < PASSES; ++p) {
+        const int c = (unit0 + i * units) * Q_BLOCK + p * (LANES * V) + c0;
+        if (c < d) {
+          if (EARLY) wv[p] = load_pack<T, V>(w + c);
+          if (res_out != nullptr) store_pack<T, V>(res_out + base + c, s[i][p]);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const double f = (double)to_f32(s[i][p].v[j]);
+          acc += f * f;
+        }
       }
-    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
     if (lane_id() == 0) part[warp_id()] = acc;
     __syncthreads();
-    if (threadIdx.x == 0) {
-      double sum = 0.0;
-      for (int i = 0; i < warps; ++i) sum += part[i];
-      r_sh = (float)(1.0 / sqrt(sum / (double)d + (double)eps));
+    if (warp_id() == 0) {
+      double sum = lane_id() < warps ? part[lane_id()] : 0.0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane_id() == 0) r_sh = (float)(1.0 / sqrt(sum / (double)d + (double)eps));
     }
     __syncthreads();
     const float r = r_sh;
-    const int unit0 = threadIdx.x / LANES, units = blockDim.x / LANES;
-    const int lane = threadIdx.x % LANES;
-    // whole warps take part in the shuffles: a unit past the last block has no columns
-    for (int b0 = 0; b0 < nb; b0 += units) {
-      const int b = b0 + unit0;
+#pragma unroll
+    for (int i = 0; i < NBW; ++i) {
+      const int b = unit0 + i * units;
       float v[PASSES][V];
       float m = 0.f;
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
-        const int c = b * Q_BLOCK + (p * LANES + lane) * V;
+        const int c = b * Q_BLOCK + p * (LANES * V) + c0;
         if (c < d) {
-          const Pack<T, V> s = load_pack<T, V>(row + c), wv = load_pack<T, V>(w + c);
+          const Pack<T, V> wc = EARLY ? wv[p] : load_pack<T, V>(w + c);
           Pack<T, V> o;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            v[p][j] = __fmul_rn(__fmul_rn(to_f32(s.v[j]), r), to_f32(wv.v[j]));
+            v[p][j] = __fmul_rn(__fmul_rn(to_f32(s[i][p].v[j]), r), to_f32(wc.v[j]));
             m = fmaxf(m, fabsf(v[p][j]));
             o.v[j] = from_f32<T>(v[p][j]);
           }
@@ -129,101 +151,126 @@ __global__ void __launch_bounds__(256) add_rmsnorm_kernel(const T* x, const T* r
       const float inv = __frcp_rn(scale);
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
-        const int c = b * Q_BLOCK + (p * LANES + lane) * V;
+        const int c = b * Q_BLOCK + p * (LANES * V) + c0;
         if (c < d) store_codes<V>(q + base + c, v[p], inv);
       }
-      if (lane == 0 && b < nb) q_scale[(size_t)t * nb + b] = scale;
+      if (c0 == 0 && b < nb) q_scale[(size_t)t * nb + b] = scale;
     }
-    __syncthreads();
   }
 }
 
-// 1 x 128 blocks: LANES lanes take one block of one row, one pass over the data.
-template <typename T, int V>
+// 1 x 128 blocks: LANES lanes take one block of one row, UNROLL blocks in flight.
+// WHOLE: the columns are whole blocks, so block u is the 128 elements from 128 u
+// on and no division finds its row.
+template <typename T, int V, bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
-                                                            float* __restrict__ scale, int64_t rows, int cols) {
-  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses;
+                                                            float* __restrict__ scale, int64_t units, int cols) {
+  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses, UNROLL = 4;
   const int nb = (cols + Q_BLOCK - 1) / Q_BLOCK;
-  const int64_t units = rows * nb;
-  const int per_block = blockDim.x / LANES;
   const int lane = threadIdx.x % LANES;
-  for (int64_t u0 = (int64_t)blockIdx.x * per_block; u0 < units; u0 += (int64_t)gridDim.x * per_block) {
-    const int64_t u = u0 + threadIdx.x / LANES;
-    const int64_t r = u / nb;
-    const int b = (int)(u - r * nb);
-    float v[PASSES][V];
-    float m = 0.f;
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x / LANES);
+  for (int64_t u0 = (int64_t)blockIdx.x * (blockDim.x / LANES) + threadIdx.x / LANES;
+       u0 - threadIdx.x / LANES < units; u0 += step * UNROLL) {
+    Pack<T, V> s[UNROLL][PASSES];
+    int64_t at[UNROLL];  // this lane's first element
+    int left[UNROLL];    // columns from there to the row's end
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int c = b * Q_BLOCK + (p * LANES + lane) * V;
-      if (u < units && c < cols) {
-        const Pack<T, V> s = load_pack<T, V>(x + r * cols + c);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          v[p][j] = to_f32(s.v[j]);
-          m = fmaxf(m, fabsf(v[p][j]));
-        }
+    for (int k = 0; k < UNROLL; ++k) {
+      const int64_t u = u0 + k * step;
+      if (WHOLE) {
+        at[k] = u * Q_BLOCK + lane * V;
+        left[k] = u < units ? Q_BLOCK : 0;
+      } else {
+        const int64_t r = u / nb;
+        const int c = (int)(u - r * nb) * Q_BLOCK + lane * V;
+        at[k] = r * cols + c;
+        left[k] = u < units ? cols - c : 0;
       }
-    }
-    const float sc = quant_scale(lanes_max<LANES>(m));
-    const float inv = __frcp_rn(sc);
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int c = b * Q_BLOCK + (p * LANES + lane) * V;
-      if (u < units && c < cols) store_codes<V>(q + r * cols + c, v[p], inv);
+      for (int p = 0; p < PASSES; ++p)
+        if (p * LANES * V < left[k]) s[k][p] = load_pack<T, V>(x + at[k] + p * (LANES * V));
     }
-    if (lane == 0 && u < units) scale[u] = sc;
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) {
+      float m = 0.f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (p * LANES * V < left[k]) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(s[k][p].v[j])));
+        }
+      const float sc = quant_scale(lanes_max<LANES>(m));
+      const float inv = __frcp_rn(sc);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (p * LANES * V < left[k]) {
+          float v[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = to_f32(s[k][p].v[j]);
+          store_codes<V>(q + at[k] + p * (LANES * V), v, inv);
+        }
+      if (lane == 0 && u0 + k * step < units) scale[u0 + k * step] = sc;
+    }
   }
 }
 
-// 128 x 128 blocks: a 256-thread block keeps one tile in registers.  Thread i
-// holds column group i % (128 / V) of rows i / (128 / V) + step * j.
+// The largest magnitude of a pack, NaN aside; bf16 pairs are compared as they are.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
-                                                             float* __restrict__ scale, int64_t tiles, int rows,
-                                                             int cols) {
-  constexpr int ACROSS = Q_BLOCK / V;       // threads across a tile row
-  constexpr int STEP = 256 / ACROSS;        // rows per pass
-  constexpr int PASSES = Q_BLOCK / STEP;    // 8 (V = 8), 16 (V = 4) or 64 (V = 1)
-  __shared__ float part[8];
-  const int rb = (rows + Q_BLOCK - 1) / Q_BLOCK, cb = (cols + Q_BLOCK - 1) / Q_BLOCK;
-  const int tr = threadIdx.x / ACROSS, tc = (threadIdx.x % ACROSS) * V;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t mat = tile / ((int64_t)rb * cb);
-    const int in_mat = (int)(tile - mat * rb * cb);
-    const int r0 = (in_mat / cb) * Q_BLOCK, c = (in_mat % cb) * Q_BLOCK + tc;
-    const size_t base = (size_t)mat * rows * cols;
-    Pack<T, V> s[PASSES];
+__device__ __forceinline__ float pack_amax(const Pack<T, V>& x) {
+  if constexpr (sizeof(T) == 2 && V == 8) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+    __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
     float m = 0.f;
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = r0 + tr + p * STEP;
-      if (r < rows && c < cols) {
-        s[p] = load_pack<T, V>(x + base + (size_t)r * cols + c);
-#pragma unroll
-        for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(s[p].v[j])));
-      }
-    }
-    m = lanes_max<32>(m);
-    __syncthreads();  // the previous tile's maxima have been read
-    if (lane_id() == 0) part[warp_id()] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, part[i]);
-    const float sc = quant_scale(m);
-    const float inv = __frcp_rn(sc);
-#pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      const int r = r0 + tr + p * STEP;
-      if (r < rows && c < cols) {
-        float v[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = to_f32(s[p].v[j]);
-        store_codes<V>(q + base + (size_t)r * cols + c, v, inv);
-      }
-    }
-    if (threadIdx.x == 0) scale[tile] = sc;
+    for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(x.v[j])));
+    return m;
   }
+}
+
+// 128 x 128 blocks: 512 threads keep one tile in registers, in its own type (the
+// fp32 form of a bf16 tile would leave room for two blocks per SM only).
+template <typename T, int V>
+__global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
+                                                                float* __restrict__ scale, int mats, int rows,
+                                                                int cols) {
+  constexpr int ACROSS = Q_BLOCK / V;       // threads across a tile row
+  constexpr int STEP = 512 / ACROSS;        // rows per pass
+  constexpr int PASSES = Q_BLOCK / STEP;    // 4 (V = 8), 8 (V = 4) or 32 (V = 1)
+  __shared__ float part[2][16];
+  const int rb = (rows + Q_BLOCK - 1) / Q_BLOCK, cb = gridDim.x;
+  const int tr = threadIdx.x / ACROSS;
+  const int c = blockIdx.x * Q_BLOCK + (threadIdx.x % ACROSS) * V;
+  int parity = 0;
+  for (int mat = blockIdx.z; mat < mats; mat += gridDim.z)
+    for (int br = blockIdx.y; br < rb; br += gridDim.y, parity ^= 1) {
+      const size_t at = ((size_t)mat * rows + br * Q_BLOCK + tr) * cols + c;
+      const int left = c < cols ? rows - br * Q_BLOCK - tr : 0;  // rows from this thread's first on
+      Pack<T, V> s[PASSES];
+      float m = 0.f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (p * STEP < left) s[p] = load_pack<T, V>(x + at + (size_t)p * STEP * cols);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (p * STEP < left) m = fmaxf(m, pack_amax<T, V>(s[p]));
+      m = lanes_max<32>(m);
+      if (lane_id() == 0) part[parity][warp_id()] = m;
+      __syncthreads();
+      m = lanes_max<16>(part[parity][lane_id() & 15]);
+      const float sc = quant_scale(m);
+      const float inv = __frcp_rn(sc);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p)
+        if (p * STEP < left) {
+          float v[V];
+#pragma unroll
+          for (int j = 0; j < V; ++j) v[j] = to_f32(s[p].v[j]);
+          store_codes<V>(q + at + (size_t)p * STEP * cols, v, inv);
+        }
+      if (threadIdx.x == 0) scale[((size_t)mat * rb + br) * cb + blockIdx.x] = sc;
+    }
 }
 
 }  // namespace moe
@@ -233,13 +280,20 @@ namespace moe_host {
 template <typename T, int V>
 static moe_status add_rmsnorm_t(const void* x, const void* residual, const void* w, void* res_out, void* xn,
                                 uint8_t* q, float* q_scale, int n, int d, float eps, cudaStream_t s) {
-  static SmemLimit lim;
-  const int smem = (int)((size_t)d * sizeof(T));
-  const moe_status st = ensure_smem_limit(moe::add_rmsnorm_kernel<T, V>, smem, lim);
-  if (st != MOE_OK) return st;
+  constexpr int LANES = moe::BlockLanes<V>::kLanes;
+  const int nb = q_blocks(d);
   const int grid = n < sm_count() * 16 ? n : sm_count() * 16;
-  moe::add_rmsnorm_kernel<T, V><<<grid, 256, smem, s>>>((const T*)x, (const T*)residual, (const T*)w, (T*)res_out,
-                                                        (T*)xn, q, q_scale, n, d, eps);
+  // blocks of 128 columns per LANES lanes: 1 while there are at most two rows per
+  // SM and the row fits 1024 threads, else 4, else 12 (d up to 49152)
+  auto threads = [&](int nbw) { return ((nb + nbw - 1) / nbw * LANES + 31) / 32 * 32; };
+  const int nbw = n <= 2 * sm_count() && threads(1) <= 1024 ? 1 : threads(4) <= 1024 ? 4 : 12;
+#define MOE_ADD_RMSNORM(NBW)                                                                                   \
+  moe::add_rmsnorm_kernel<T, V, NBW><<<grid, threads(NBW), 0, s>>>((const T*)x, (const T*)residual, (const T*)w, \
+                                                                   (T*)res_out, (T*)xn, q, q_scale, n, d, eps)
+  if (nbw == 1) MOE_ADD_RMSNORM(1);
+  else if (nbw == 4) MOE_ADD_RMSNORM(4);
+  else MOE_ADD_RMSNORM(12);
+#undef MOE_ADD_RMSNORM
   return launch_status();
 }
 
@@ -260,18 +314,18 @@ template <typename T, int V>
 static moe_status quantize_t(int block_rows, int mats, int rows, int cols, const void* x, uint8_t* q, float* scale,
                              cudaStream_t s) {
   const int nb = q_blocks(cols);
-  const int64_t most = (int64_t)sm_count() * 8;
   if (block_rows == 1) {
-    const int64_t all = (int64_t)mats * rows;
-    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes;
-    const int64_t blocks = (all * nb + per_block - 1) / per_block;
-    moe::quantize_rows_kernel<T, V><<<(unsigned)(blocks < most ? blocks : most), 256, 0, s>>>((const T*)x, q, scale,
-                                                                                              all, cols);
+    const int64_t units = (int64_t)mats * rows * nb;
+    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes * 4;  // four blocks in flight per lane group
+    const int64_t blocks = std::min<int64_t>((units + per_block - 1) / per_block, 0x7fffffff);
+    if (V > 1 && cols % moe::Q_BLOCK == 0)
+      moe::quantize_rows_kernel<T, V, true><<<(unsigned)blocks, 256, 0, s>>>((const T*)x, q, scale, units, cols);
+    else
+      moe::quantize_rows_kernel<T, V, false><<<(unsigned)blocks, 256, 0, s>>>((const T*)x, q, scale, units, cols);
     return launch_status();
   }
-  const int64_t tiles = (int64_t)mats * q_blocks(rows) * nb;
-  moe::quantize_tiles_kernel<T, V><<<(unsigned)(tiles < most ? tiles : most), 256, 0, s>>>((const T*)x, q, scale,
-                                                                                           tiles, rows, cols);
+  const dim3 grid((unsigned)nb, (unsigned)std::min(q_blocks(rows), 65535), (unsigned)std::min(mats, 65535));
+  moe::quantize_tiles_kernel<T, V><<<grid, 512, 0, s>>>((const T*)x, q, scale, mats, rows, cols);
   return launch_status();
 }
 
