@@ -693,7 +693,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           }
           return true;
         };
-        auto claim = [&]() -> int { return step + atomicAdd(args.hdr + F_CLAIM_WORD, 1); };
+        // (no tiles to claim where every pair has at most one)
+        const bool claims = total_tiles > step;
+        auto claim = [&]() -> int { return claims ? step + atomicAdd(args.hdr + F_CLAIM_WORD, 1) : total_tiles; };
         int t = first;
         int pending = 0;  // even CTA: the claimed successor of the next tile
         if (leader) {
@@ -775,7 +777,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           // every pair has made its last claim before the last one to get here
           // clears the counter for the next launch
           __threadfence();
-          if (atomicAdd(args.hdr + F_DONE_WORD, 1) == step - 1) {
+          if (claims && atomicAdd(args.hdr + F_DONE_WORD, 1) == step - 1) {
             atomicExch(args.hdr + F_CLAIM_WORD, 0);
             atomicExch(args.hdr + F_DONE_WORD, 0);
           }
@@ -940,7 +942,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const float2 x = unpack64(a[2 * i]), y = unpack64(a[2 * i + 1]);
         __stcg(mine + i * 256, make_float4(x.x, x.y, y.x, y.y));
       }
-      __threadfence();
       __syncwarp();
       if (lane == 0) mbar_arrive(&split_bar);
       const uint32_t ph = split_phase;
@@ -950,9 +951,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (leader) {
           if (!f8_warp_wait<true>(&pair_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
           if (lane == 0) {
-            __threadfence();
+            __threadfence();  // after the barriers: for every thread of the pair's epilogues
             const bool last = atomicInc(args.split_count + tl.index, (unsigned)args.splits - 1u) ==
                               (unsigned)args.splits - 1u;  // and back to zero for the next launch
+            __threadfence();
             last_sh = last;
             mbar_arrive(&done_bar);
             const uint32_t peer_done = map_to_rank(&done_bar, 1);
@@ -960,14 +962,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             st_async_b32(map_to_rank((const void*)&last_sh, 1), last, peer_done);
           }
         } else if (lane == 0) {
-          __threadfence();
-          mbar_arrive_cluster(map_to_rank(&pair_bar, 0));
+          mbar_arrive_cluster(map_to_rank(&pair_bar, 0));  // releases this CTA's stores to the even CTA
         }
         __syncwarp();
       }
       if (!f8_warp_wait<true>(&done_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
       if (!last_sh) return 1;
-      __threadfence();
 #pragma unroll
       for (int i = 0; i < 64; ++i) a[i] = 0ull;
 #pragma unroll
