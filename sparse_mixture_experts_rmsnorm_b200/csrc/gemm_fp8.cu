@@ -77,7 +77,12 @@ constexpr int F_SLOTS = 2;                            // rows of scale products,
 // readers of a published tile index: even CTA: MMA, 2 scale and 8 epilogue
 // warps; odd CTA: producer, 2 and 8
 constexpr int F_TRING_READERS = 22;
-constexpr int F_WIDE_ROWS = 96;                       // rows a group from which on the wide tiling is taken
+// Rows a group from which on the wide tiling is taken.  It reads its accumulators
+// faster but works on 256 rows whatever a group has.  Expert FFN of 7168 x 2048 (or
+// 4096 x 14336) in a steady loop, wide against swapped: 128 rows a group 507 and
+// 461 us, 141 rows 1002 and 948, 256 rows 5464 and 5482 (both at the power limit),
+// 1024 rows 1939 and 2290.
+constexpr int F_WIDE_ROWS = 256;
 constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's output block of 64-byte rows
 constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;         // swapped: 16 rows of 32 bf16
 constexpr int F_OUT_WIDE_BYTES = 32 * F_OUT_PITCH;    // wide: 32 rows

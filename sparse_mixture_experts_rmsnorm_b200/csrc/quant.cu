@@ -61,11 +61,93 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
+// Many rows: one block of up to 256 threads per row (grid-stride), the row s staged
+// in shared memory in its own type; every warp takes whole blocks of 128 columns
+// in the second pass, so a scale needs no shared memory.  Bound by HBM; few
+// registers keep many rows in flight: 8192 rows of 7168 bf16 columns with residual
+// and every output move at 5.7 TB/s, the register form below at 4.9 at most.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) add_rmsnorm_staged_kernel(const T* x, const T* residual, const T* __restrict__ w,
+                                                          T* res_out, T* xn, uint8_t* __restrict__ q,
+                                                          float* __restrict__ q_scale, int n, int d, float eps) {
+  extern __shared__ __align__(16) uint8_t row_raw[];
+  T* row = reinterpret_cast<T*>(row_raw);
+  __shared__ double part[8];
+  __shared__ float r_sh;
+  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses;
+  const int warps = blockDim.x >> 5;
+  const int nb = (d + Q_BLOCK - 1) / Q_BLOCK;
+  for (int t = blockIdx.x; t < n; t += gridDim.x) {
+    const size_t base = (size_t)t * d;
+    double acc = 0.0;
+    for (int i = threadIdx.x * V; i < d; i += blockDim.x * V) {
+      Pack<T, V> s = load_pack<T, V>(x + base + i);
+      if (residual != nullptr) {
+        const Pack<T, V> b = load_pack<T, V>(residual + base + i);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s.v[j] = from_f32<T>(__fadd_rn(to_f32(s.v[j]), to_f32(b.v[j])));
+      }
+      if (res_out != nullptr) store_pack<T, V>(res_out + base + i, s);
+      store_pack<T, V>(row + i, s);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const double f = (double)to_f32(s.v[j]);
+        acc += f * f;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    if (lane_id() == 0) part[warp_id()] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      double sum = 0.0;
+      for (int i = 0; i < warps; ++i) sum += part[i];
+      r_sh = (float)(1.0 / sqrt(sum / (double)d + (double)eps));
+    }
+    __syncthreads();
+    const float r = r_sh;
+    const int unit0 = threadIdx.x / LANES, units = blockDim.x / LANES;
+    const int lane = threadIdx.x % LANES;
+    // whole warps take part in the shuffles: a unit past the last block has no columns
+    for (int b0 = 0; b0 < nb; b0 += units) {
+      const int b = b0 + unit0;
+      float v[PASSES][V];
+      float m = 0.f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int c = b * Q_BLOCK + (p * LANES + lane) * V;
+        if (c < d) {
+          const Pack<T, V> s = load_pack<T, V>(row + c), wv = load_pack<T, V>(w + c);
+          Pack<T, V> o;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            v[p][j] = __fmul_rn(__fmul_rn(to_f32(s.v[j]), r), to_f32(wv.v[j]));
+            m = fmaxf(m, fabsf(v[p][j]));
+            o.v[j] = from_f32<T>(v[p][j]);
+          }
+          if (xn != nullptr) store_pack<T, V>(xn + base + c, o);
+        }
+      }
+      if (q == nullptr) continue;
+      const float scale = quant_scale(lanes_max<LANES>(m));
+      const float inv = __frcp_rn(scale);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        const int c = b * Q_BLOCK + (p * LANES + lane) * V;
+        if (c < d) store_codes<V>(q + base + c, v[p], inv);
+      }
+      if (lane == 0 && b < nb) q_scale[(size_t)t * nb + b] = scale;
+    }
+    __syncthreads();
+  }
+}
+
 // One block per row (grid-stride), the row in registers: LANES lanes hold NBW
 // blocks of 128 columns, UNITS apart, so that every sum and every block's largest
-// magnitude is a few shuffles away.  Bound by HBM: each input is read once, each
-// output written once.  With few rows NBW is 1 and the row is spread over up to
-// 1024 threads (latency); else NBW = 4, so that a thread has 8 loads in flight.
+// magnitude is a few shuffles away.  For few rows (NBW = 1 spreads a row of up to
+// 1024 LANES lanes over one block: latency) and for odd widths (V = 1), where it has
+// more loads in flight than the staged form: 2048 rows of 5003 fp32 columns, 37
+// against 45 us.
 template <typename T, int V, int NBW>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ w,
                                                            T* res_out, T* xn, uint8_t* __restrict__ q,
@@ -159,58 +241,61 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
   }
 }
 
-// 1 x 128 blocks: LANES lanes take one block of one row, UNROLL blocks in flight.
+template <bool WHOLE>
+constexpr int kUnroll = WHOLE ? 4 : 2;
+
+// 1 x 128 blocks: LANES lanes take one block of one row, UNROLL of them in flight;
+// a thread block takes consecutive ones (4096 x 14336 bf16: 35 us, 5.0 TB/s; with its
+// blocks a grid's width apart 43 us).
 // WHOLE: the columns are whole blocks, so block u is the 128 elements from 128 u
 // on and no division finds its row.
 template <typename T, int V, bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                             float* __restrict__ scale, int64_t units, int cols) {
-  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses, UNROLL = 4;
+  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses, UNROLL = kUnroll<WHOLE>;
   const int nb = (cols + Q_BLOCK - 1) / Q_BLOCK;
   const int lane = threadIdx.x % LANES;
-  const int64_t step = (int64_t)gridDim.x * (blockDim.x / LANES);
-  for (int64_t u0 = (int64_t)blockIdx.x * (blockDim.x / LANES) + threadIdx.x / LANES;
-       u0 - threadIdx.x / LANES < units; u0 += step * UNROLL) {
-    Pack<T, V> s[UNROLL][PASSES];
-    int64_t at[UNROLL];  // this lane's first element
-    int left[UNROLL];    // columns from there to the row's end
+  const int across = blockDim.x / LANES;  // blocks of 128 columns that the thread block takes at once
+  const int64_t u0 = (int64_t)blockIdx.x * across * UNROLL + threadIdx.x / LANES;
+  Pack<T, V> s[UNROLL][PASSES];
+  int64_t at[UNROLL];  // this lane's first element
+  int left[UNROLL];    // columns from there to the row's end
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      const int64_t u = u0 + k * step;
-      if (WHOLE) {
-        at[k] = u * Q_BLOCK + lane * V;
-        left[k] = u < units ? Q_BLOCK : 0;
-      } else {
-        const int64_t r = u / nb;
-        const int c = (int)(u - r * nb) * Q_BLOCK + lane * V;
-        at[k] = r * cols + c;
-        left[k] = u < units ? cols - c : 0;
+  for (int k = 0; k < UNROLL; ++k) {
+    const int64_t u = u0 + k * across;
+    if (WHOLE) {
+      at[k] = u * Q_BLOCK + lane * V;
+      left[k] = u < units ? Q_BLOCK : 0;
+    } else {
+      const int64_t r = u / nb;
+      const int c = (int)(u - r * nb) * Q_BLOCK + lane * V;
+      at[k] = r * cols + c;
+      left[k] = u < units ? cols - c : 0;
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+      if (p * LANES * V < left[k]) s[k][p] = load_pack<T, V>(x + at[k] + p * (LANES * V));
+  }
+#pragma unroll
+  for (int k = 0; k < UNROLL; ++k) {
+    float m = 0.f;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p)
+      if (p * LANES * V < left[k]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(s[k][p].v[j])));
       }
+    const float sc = quant_scale(lanes_max<LANES>(m));
+    const float inv = __frcp_rn(sc);
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p)
-        if (p * LANES * V < left[k]) s[k][p] = load_pack<T, V>(x + at[k] + p * (LANES * V));
-    }
+    for (int p = 0; p < PASSES; ++p)
+      if (p * LANES * V < left[k]) {
+        float v[V];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      float m = 0.f;
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p)
-        if (p * LANES * V < left[k]) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(s[k][p].v[j])));
-        }
-      const float sc = quant_scale(lanes_max<LANES>(m));
-      const float inv = __frcp_rn(sc);
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p)
-        if (p * LANES * V < left[k]) {
-          float v[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) v[j] = to_f32(s[k][p].v[j]);
-          store_codes<V>(q + at[k] + p * (LANES * V), v, inv);
-        }
-      if (lane == 0 && u0 + k * step < units) scale[u0 + k * step] = sc;
-    }
+        for (int j = 0; j < V; ++j) v[j] = to_f32(s[k][p].v[j]);
+        store_codes<V>(q + at[k] + p * (LANES * V), v, inv);
+      }
+    if (lane == 0 && u0 + k * across < units) scale[u0 + k * across] = sc;
   }
 }
 
@@ -283,16 +368,27 @@ static moe_status add_rmsnorm_t(const void* x, const void* residual, const void*
   constexpr int LANES = moe::BlockLanes<V>::kLanes;
   const int nb = q_blocks(d);
   const int grid = n < sm_count() * 16 ? n : sm_count() * 16;
-  // blocks of 128 columns per LANES lanes: 1 while there are at most two rows per
-  // SM and the row fits 1024 threads, else 4, else 12 (d up to 49152)
+  // threads of the register form with nbw blocks of 128 columns per LANES lanes
   auto threads = [&](int nbw) { return ((nb + nbw - 1) / nbw * LANES + 31) / 32 * 32; };
-  const int nbw = n <= 2 * sm_count() && threads(1) <= 1024 ? 1 : threads(4) <= 1024 ? 4 : 12;
+  const bool few = n <= 2 * sm_count() && threads(1) <= 1024;
 #define MOE_ADD_RMSNORM(NBW)                                                                                   \
   moe::add_rmsnorm_kernel<T, V, NBW><<<grid, threads(NBW), 0, s>>>((const T*)x, (const T*)residual, (const T*)w, \
                                                                    (T*)res_out, (T*)xn, q, q_scale, n, d, eps)
-  if (nbw == 1) MOE_ADD_RMSNORM(1);
-  else if (nbw == 4) MOE_ADD_RMSNORM(4);
-  else MOE_ADD_RMSNORM(12);
+  if (few) {
+    MOE_ADD_RMSNORM(1);
+  } else if constexpr (V == 1) {
+    if (threads(4) <= 1024) MOE_ADD_RMSNORM(4);
+    else MOE_ADD_RMSNORM(12);  // d up to 49152
+  } else {
+    static SmemLimit lim;
+    const int smem = (int)((size_t)d * sizeof(T));
+    const moe_status st = ensure_smem_limit(moe::add_rmsnorm_staged_kernel<T, V>, smem, lim);
+    if (st != MOE_OK) return st;
+    // about four passes over the row, 64 to 192 threads
+    const int t = std::min(192, std::max(64, (d / V + 127) / 128 * 32));
+    moe::add_rmsnorm_staged_kernel<T, V><<<grid, t, smem, s>>>((const T*)x, (const T*)residual, (const T*)w,
+                                                               (T*)res_out, (T*)xn, q, q_scale, n, d, eps);
+  }
 #undef MOE_ADD_RMSNORM
   return launch_status();
 }
@@ -316,9 +412,11 @@ static moe_status quantize_t(int block_rows, int mats, int rows, int cols, const
   const int nb = q_blocks(cols);
   if (block_rows == 1) {
     const int64_t units = (int64_t)mats * rows * nb;
-    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes * 4;  // four blocks in flight per lane group
-    const int64_t blocks = std::min<int64_t>((units + per_block - 1) / per_block, 0x7fffffff);
-    if (V > 1 && cols % moe::Q_BLOCK == 0)
+    const bool whole = V > 1 && cols % moe::Q_BLOCK == 0;
+    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes * (whole ? moe::kUnroll<true> : moe::kUnroll<false>);
+    const int64_t blocks = (units + per_block - 1) / per_block;
+    if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+    if (whole)
       moe::quantize_rows_kernel<T, V, true><<<(unsigned)blocks, 256, 0, s>>>((const T*)x, q, scale, units, cols);
     else
       moe::quantize_rows_kernel<T, V, false><<<(unsigned)blocks, 256, 0, s>>>((const T*)x, q, scale, units, cols);

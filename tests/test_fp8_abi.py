@@ -38,6 +38,14 @@ def test_workspace_size_holds_the_documented_regions():
         moe.workspace_fp8(_cfg(top_k=9))
 
 
+def test_few_tiles_have_room_for_their_parts():
+    """Partial sums of products with few tiles; none where the tiles alone fill the GPU."""
+    size = lib.moe_workspace_size_gemm_fp8
+    assert size(1, 1, 4096, 7168) > 1 << 20
+    assert size(1, 8192, 4096, 7168) == 1024 == size(64, 9000, 2048, 7168)
+    assert size(1, 1, 4096, 128) == 1024  # a single block along K is not cut
+
+
 def test_norm_refusals():
     def norm(cfg=None, x=256, res=None, w=256, res_out=256, xn=256, q=None, s=None):
         return lib.moe_add_rmsnorm(ctypes.byref((cfg or _cfg()).c()), x, res, w, res_out, xn, q, s, None)
@@ -72,7 +80,7 @@ def test_gemm_refusals():
     assert gemm(k=264) == UNSUPPORTED and gemm(a=264) == UNSUPPORTED and gemm(b=257) == UNSUPPORTED
     assert gemm(lda=240) == BAD and gemm(lda=264) == UNSUPPORTED
     assert gemm(g=1024, offs=256, n=1 << 22) == UNSUPPORTED
-    assert gemm(bytes=128) == WORKSPACE
+    assert gemm(bytes=1023) == WORKSPACE
     assert gemm(rows=0, a=None, sa=None, b=None, sb=None, c=None) == moe.MOE_OK
 
 

@@ -38,7 +38,7 @@ def _close(got, want, slack, out):
 
 # ---------------------------------------------------------------- norm
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n,d", [(0, 64), (1, 1), (1, 7168), (3, 127), (5, 128), (2, 129), (300, 1000), (64, 7168),
+@pytest.mark.parametrize("n,d", [(0, 64), (300, 7168), (320, 4097), (2, 40001), (301, 20001), (1, 1), (1, 7168), (3, 127), (5, 128), (2, 129), (300, 1000), (64, 7168),
                                  (7, 4099), (2, 16384), (2, 49152), (2500, 256)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_add_rmsnorm(env, dtype, n, d, residual):
@@ -168,7 +168,8 @@ def _offsets(torch, sizes):
 @pytest.mark.parametrize("rows,n,k", [(1, 1, 16), (1, 4096, 7168), (2, 7, 48), (17, 130, 144), (64, 256, 128),
                                       (128, 128, 256), (129, 384, 272), (256, 512, 1024), (257, 300, 2048),
                                       (333, 1111, 1040), (1000, 264, 640), (2048, 2048, 512), (48, 7168, 2048),
-                                      (16, 257, 7168)])
+                                      (16, 257, 7168), (1, 1, 7168), (300, 256, 4096), (513, 130, 2064), (255, 512, 128),
+                                      (3, 100, 16400)])
 def test_gemm(env, out, rows, n, k):
     torch, moe = env
     aq, as_, bq, bs = _operands(torch, [rows], n, k)
@@ -193,6 +194,7 @@ GROUPS = {
     "one large": [3, 1500, 4, 0],
     "many small": [(7 * i) % 5 for i in range(200)],
     "the most groups": [1] * 1024,
+    "large and ragged": [300, 0, 520, 257, 400],
 }
 
 
@@ -213,6 +215,27 @@ def test_grouped_gemm(env, out, name, n, k):
     moe.moe_gemm_fp8(g, _offsets(torch, sizes), rows + spare, n, k, aq, as_, bq, bs, out, c, ws)
     _close(c[:rows], want[:rows], mag[:rows] * U32 * (k + 32), out)
     assert torch.all(c[rows:] == 7.0)  # rows behind the last group are left as they were
+    assert moe.moe_check_device_error(ws)[0] == 0
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("sizes,n,k", [([5, 9], 256, 2048), ([0, 3, 0], 300, 4096), ([400, 300], 200, 2048),
+                                       ([0, 0], 256, 2048)])
+def test_few_tiles_cut_along_k(env, out, sizes, n, k):
+    """Products of few tiles, whose parts along K meet in the workspace: the values, and the same bits every time."""
+    torch, moe = env
+    g, rows = len(sizes), sum(sizes) + 4
+    assert moe.library().moe_workspace_size_gemm_fp8(g, rows, n, k) > 4096  # parts are held
+    aq, as_, bq, bs = _operands(torch, sizes + [4], n, k, g)
+    want, mag = f8.product(f8.values(aq, as_, 1), f8.values(bq, bs, 128), sizes)
+    ws = moe.workspace_gemm_fp8(g, rows, n, k)
+    c = torch.full((4, rows, n), 7.0, dtype=_type(torch, out), device="cuda")
+    for i in range(4):
+        moe.moe_gemm_fp8(g, _offsets(torch, sizes), rows, n, k, aq, as_, bq, bs, out, c[i], ws)
+        assert torch.equal(c[i], c[0])
+    m = sum(sizes)
+    _close(c[0, :m], want[:m], mag[:m] * U32 * (k + 32), out)
+    assert torch.all(c[:, m:] == 7.0)
     assert moe.moe_check_device_error(ws)[0] == 0
 
 
@@ -297,7 +320,8 @@ def _ffn_want(torch, x, gate, up, down, sizes):
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("sizes,d,h", [([1], 128, 128), ([40], 256, 384), ([3, 0, 70, 300], 512, 256),
                                        ([5, 260, 1], 272, 208), ([700], 1024, 144), ([0, 2], 144, 16),
-                                       ([(3 * i) % 4 for i in range(40)], 256, 320)])
+                                       ([(3 * i) % 4 for i in range(40)], 256, 320), ([300, 0, 520, 260], 256, 208),
+                                       ([1], 7168, 256), ([300], 2048, 256), ([2, 0, 3], 2048, 128)])
 def test_expert_ffn(env, out, sizes, d, h):
     torch, moe = env
     g, rows, spare = len(sizes), sum(sizes), 3
@@ -466,6 +490,41 @@ def test_graph_capture_and_other_stream(env):
     moe.moe_layer_forward_fp8(cfg, w, h, res, bias, ref, ws)
     assert torch.equal(out, ref)
     assert moe.moe_check_device_error(ws)[0] == 0
+
+
+def test_two_calls_at_once_and_two_graphs_on_one_workspace(env):
+    """Products on two streams, each with its own workspace, and two captured graphs that share one."""
+    torch, moe = env
+    cases = [(1, 512, 4096), (300, 256, 2048), (700, 1024, 512)]
+    ops = [_operands(torch, [r], n, k) for r, n, k in cases]
+    ref = []
+    for (r, n, k), o in zip(cases, ops):
+        ref.append(torch.empty(r, n, device="cuda"))
+        moe.moe_gemm_fp8(1, None, r, n, k, *o, "f32", ref[-1], moe.workspace_gemm_fp8(1, r, n, k))
+    torch.cuda.synchronize()
+    got = [torch.empty_like(x) for x in ref]
+    spaces = [moe.workspace_gemm_fp8(1, *c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (r, n, k), o, c, ws, st in zip(cases, ops, got, spaces, streams):
+            moe.moe_gemm_fp8(1, None, r, n, k, *o, "f32", c, ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
+    size = max(w.numel() for w in spaces)
+    shared = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert moe.library().moe_workspace_init(shared.data_ptr(), size, None) == 0
+    torch.cuda.synchronize()
+    graphs = []
+    for (r, n, k), o, c in zip(cases, ops, got):
+        c.zero_()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            moe.moe_gemm_fp8(1, None, r, n, k, *o, "f32", c, shared)
+    for i in (0, 1, 2, 1, 0, 2, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
 @pytest.mark.parametrize("name", ["folded shared expert", "separate shared expert, capacity", "fp32"])
