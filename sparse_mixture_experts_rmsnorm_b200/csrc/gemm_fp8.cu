@@ -85,7 +85,7 @@ constexpr int F_TRING_READERS = 22;
 constexpr int F_WIDE_ROWS = 256;
 constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's output block of 64-byte rows
 constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;         // swapped: 16 rows of 32 bf16
-constexpr int F_OUT_WIDE_BYTES = 32 * F_OUT_PITCH;    // wide: 32 rows
+constexpr int F_OUT_WIDE_BYTES = 2048;                // wide: 16 rows of 128 bytes, or 32 of 64
 constexpr int F_CLAIM_WORD = 40, F_DONE_WORD = 41;    // header words: tiles claimed, pairs finished
 
 // Rows of scale products per slot of 256 (swapped), and floats of a slot.
@@ -528,32 +528,43 @@ __device__ __forceinline__ bool f8_pass_over(Fp8Drain& d, int nk, const Fp8Args&
   return true;
 }
 
-// Writes 64 bytes (w) of each of the warp's 32 rows, lane = row, to C: row r at
+// Writes BYTES (w) of each of the warp's 32 rows, lane = row, to C: row r at
 // c + r * ld, `valid` rows, of which the first `bytes` bytes exist.  Through the
-// warp's block of shared memory, so that a store instruction writes whole
-// 64-byte pieces of eight rows.  vec: c, ld and bytes are multiples of 16.
-template <int ES>
-__device__ __forceinline__ void f8_store_rows(uint8_t* stage, const uint4 (&w)[4], uint8_t* c, size_t ld, int valid,
-                                              int bytes, bool vec) {
+// warp's block of shared memory (16 rows of 128 bytes at a time, or 32 of 64), so
+// that the stores write whole 128-byte lines: they go out by the line, and 64-byte
+// pieces of eight rows per instruction took about twice as long.
+// vec: c, ld and bytes are multiples of 16; else elements of ES bytes.
+template <int ES, int BYTES>
+__device__ __forceinline__ void f8_store_rows(uint8_t* block, const uint4 (&w)[BYTES / 16], uint8_t* c, size_t ld,
+                                              int valid, int bytes, bool vec) {
+  constexpr int ROWS = F_OUT_WIDE_BYTES / BYTES, PIECES = BYTES / 16;
   const int lane = lane_id();
-  __syncwarp();
+  // 16-byte piece i of a row lies where no two of eight rows meet in a bank
+  auto at = [&](int r, int i) {
+    return block + r * BYTES + ((BYTES == 128 ? i ^ (r & 7) : i ^ ((r >> 1) & 3)) << 4);
+  };
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(stage + lane * F_OUT_PITCH + i * 16) = w[i];
-  __syncwarp();
-  if (vec) {
+  for (int r0 = 0; r0 < 32; r0 += ROWS) {
+    __syncwarp();
+    if (lane >= r0 && lane < r0 + ROWS) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2), at = (lane & 3) * 16;
-      const uint4 q = *reinterpret_cast<const uint4*>(stage + r * F_OUT_PITCH + at);
-      if (r < valid && at < bytes) *reinterpret_cast<uint4*>(c + (size_t)r * ld + at) = q;
+      for (int i = 0; i < PIECES; ++i) *reinterpret_cast<uint4*>(at(lane - r0, i)) = w[i];
     }
-  } else {
-    constexpr int COLS = 64 / ES;
-    for (int i = lane; i < 32 * COLS; i += 32) {
-      const int r = i / COLS, at = (i % COLS) * ES;
-      if (r < valid && at < bytes) {
-        if (ES == 4) *reinterpret_cast<float*>(c + (size_t)r * ld + at) = *reinterpret_cast<const float*>(stage + r * F_OUT_PITCH + at);
-        else *reinterpret_cast<bf16*>(c + (size_t)r * ld + at) = *reinterpret_cast<const bf16*>(stage + r * F_OUT_PITCH + at);
+    __syncwarp();
+    if (vec) {
+#pragma unroll
+      for (int i = 0; i < ROWS * PIECES / 32; ++i) {
+        const int r = i * (32 / PIECES) + lane / PIECES, p = lane % PIECES;
+        const uint4 q = *reinterpret_cast<const uint4*>(at(r, p));
+        if (r0 + r < valid && p * 16 < bytes) *reinterpret_cast<uint4*>(c + (size_t)(r0 + r) * ld + p * 16) = q;
+      }
+    } else if constexpr (ES > 1) {
+      using T = typename std::conditional<ES == 4, float, bf16>::type;
+      constexpr int COLS = BYTES / ES;
+      for (int i = lane; i < ROWS * COLS; i += 32) {
+        const int r = i / COLS, b = (i % COLS) * ES;
+        if (r0 + r < valid && b < bytes)
+          *reinterpret_cast<T*>(c + (size_t)(r0 + r) * ld + b) = *reinterpret_cast<const T*>(at(r, b / 16) + b % 16);
       }
     }
   }
@@ -1021,29 +1032,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                          (warp - F_EPI_WARP0) * F_OUT_WIDE_BYTES;
         const size_t row = (size_t)tl.row0 + (int)rank * 128 + r_cta;
         if constexpr (!SWIGLU) {
-          constexpr int ES = EPI == moe_host::EPI_F32 ? 4 : 2, COLS = 64 / ES;
+          constexpr int ES = EPI == moe_host::EPI_F32 ? 4 : 2, COLS = 128 / ES;
           const int n0 = tl.o * 256 + hf * 128;
           const size_t ld = (size_t)args.nout * ES;
           uint8_t* c = reinterpret_cast<uint8_t*>(args.c) + row * ld + (size_t)n0 * ES;
 #pragma unroll
-          for (int p = 0; p < 128 / COLS; ++p) {  // 16 (fp32) or 32 columns per pass
+          for (int p = 0; p < 128 / COLS; ++p) {  // 32 (fp32) or 64 columns at a time
             const int left = args.nout - (n0 + p * COLS);
             if (left <= 0) break;
-            uint4 w[4];
+            uint4 w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               if constexpr (ES == 4) {
-                const float2 x = unpack64(acc[p][2 * i]), y = unpack64(acc[p][2 * i + 1]);
+                const uint64_t* a = &acc[2 * p + (i >> 2)][(i & 3) * 2];
+                const float2 x = unpack64(a[0]), y = unpack64(a[1]);
                 w[i] = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
                                   __float_as_uint(y.y));
               } else {
-                const uint64_t* a = &acc[2 * p + (i >> 1)][(i & 1) * 4];
+                const uint64_t* a = &acc[4 * p + (i >> 1)][(i & 1) * 4];
                 const float2 x = unpack64(a[0]), y = unpack64(a[1]), z = unpack64(a[2]), q = unpack64(a[3]);
                 w[i] = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y), pack_bf16x2(z.x, z.y),
                                   pack_bf16x2(q.x, q.y));
               }
             }
-            f8_store_rows<ES>(stage, w, c + p * 64, ld, valid, left * ES, args.vec);
+            f8_store_rows<ES, 128>(stage, w, c + p * 128, ld, valid, left * ES, args.vec);
           }
         } else {
           const bool up_first = tl.group == args.shared_group ? args.s_up_first : args.up_first;
@@ -1085,7 +1097,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             w[i] = make_uint4(q[0], q[1], q[2], q[3]);
           }
           if (unit0 < args.nout)
-            f8_store_rows<1>(stage, w, reinterpret_cast<uint8_t*>(args.c) + row * args.nout + unit0, args.nout, valid,
+            f8_store_rows<1, 64>(stage, w, reinterpret_cast<uint8_t*>(args.c) + row * args.nout + unit0, args.nout, valid,
                              args.nout - unit0, true);
         }
       } else {
