@@ -335,9 +335,14 @@ __device__ __forceinline__ int f8_scale_at(int c) {
   return (c & ~15) + ((c & 6) << 1) + ((c & 8) >> 2) + (c & 1);
 }
 
-// silu(z) = z / (1 + e^-z), the fast exp and divide intrinsics: about 1e-6
-// relative error, far below the e4m3 rounding that follows.
-__device__ __forceinline__ float f8_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// silu(g) * u, silu(g) = g / (1 + e^-g), with the approximate exponential and
+// reciprocal: about 1e-6 relative error, far below the e4m3 rounding that follows.
+// Once e^-g overflows, the reciprocal is 0 and so is the result.
+__device__ __forceinline__ float f8_silu_mul(float g, float u) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  return __fmul_rn(__fmul_rn(g, r), u);
+}
 
 // Byte transpose over the four lanes l, l ^ 4, l ^ 8, l ^ 12: lane i = (l / 4) % 4
 // of them gets byte i of every lane's word, in lane order.
@@ -1060,17 +1065,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         } else {
           const bool up_first = tl.group == args.shared_group ? args.s_up_first : args.up_first;
           const int unit0 = tl.o * 128 + hf * 64;  // this warp's hidden units, 8 per 16 columns
+          // the activation in place; the order of the two matrices is the tile's, so
+          // the choice stays outside the 64 units
+          auto activate = [&](auto up_is_first) {
+            constexpr bool UP = decltype(up_is_first)::value;
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 g = unpack64(acc[b][UP ? 4 + i : i]), u = unpack64(acc[b][UP ? i : 4 + i]);
+                acc[b][i] = pack64(__float_as_uint(f8_silu_mul(g.x, u.x)), __float_as_uint(f8_silu_mul(g.y, u.y)));
+              }
+          };
+          if (up_first) activate(std::true_type());
+          else activate(std::false_type());
+          if (unit0 + 64 > args.nout) {  // units past the last one (nout is even)
+#pragma unroll
+            for (int b = 0; b < 8; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (unit0 + b * 8 + 2 * i >= args.nout) acc[b][i] = 0ull;
+          }
           float m = 0.f;
 #pragma unroll
           for (int b = 0; b < 8; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack64(acc[b][i]), y = unpack64(acc[b][4 + i]);
-              const bool in = unit0 + b * 8 + 2 * i < args.nout;  // nout is even
-              const float v0 = in ? __fmul_rn(f8_silu(up_first ? y.x : x.x), up_first ? x.x : y.x) : 0.f;
-              const float v1 = in ? __fmul_rn(f8_silu(up_first ? y.y : x.y), up_first ? x.y : y.y) : 0.f;
-              m = fmaxf(m, fmaxf(fabsf(v0), fabsf(v1)));
-              acc[b][i] = pack64(__float_as_uint(v0), __float_as_uint(v1));
+              const float2 v = unpack64(acc[b][i]);
+              m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
             }
           // the other half of the row's 128 units is with the warp of the same rows.
           // Two buffers: that warp reads this tile's value before it arrives for the next.
@@ -1193,8 +1215,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
               for (int l16 = 0; l16 < 2; ++l16) {
                 const float2 p = unpack64(acc[b][l16][j][0]), q = unpack64(acc[b][l16][j][1]);
                 const bool in = unit0 + l16 * 8 + (lane >> 2) < args.nout;
-                const float vx = in ? __fmul_rn(f8_silu(up_first ? q.x : p.x), up_first ? p.x : q.x) : 0.f;
-                const float vy = in ? __fmul_rn(f8_silu(up_first ? q.y : p.y), up_first ? p.y : q.y) : 0.f;
+                const float vx = in ? f8_silu_mul(up_first ? q.x : p.x, up_first ? p.x : q.x) : 0.f;
+                const float vy = in ? f8_silu_mul(up_first ? q.y : p.y, up_first ? p.y : q.y) : 0.f;
                 mx = fmaxf(mx, fabsf(vx));
                 my = fmaxf(my, fabsf(vy));
                 acc[b][l16][j][0] = pack64(__float_as_uint(vx), __float_as_uint(vy));
