@@ -339,8 +339,9 @@ __device__ __forceinline__ int f8_scale_at(int c) {
 // reciprocal: about 1e-6 relative error, far below the e4m3 rounding that follows.
 // Once e^-g overflows, the reciprocal is 0 and so is the result.
 __device__ __forceinline__ float f8_silu_mul(float g, float u) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-g)));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return __fmul_rn(__fmul_rn(g, r), u);
 }
 
