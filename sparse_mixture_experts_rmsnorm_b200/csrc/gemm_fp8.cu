@@ -41,9 +41,10 @@
 //   warps 2, 3  scale products, one warp per TMEM slot;
 //   warps 4-11  epilogue: warp w holds TMEM lanes 32 (w % 4) .. + 31 and one half
 //               of the tile's columns.
-// Few tiles (a handful of rows): each is cut along K into `splits` parts, so that
-// the weights stream through all SMs; the parts' fp32 sums meet in the workspace
-// and the CTA that comes last adds them in order and writes the result.
+// Few tiles (a handful of rows): chunks get smaller, or each tile is cut along K
+// into `splits` parts, so that the weights stream through all SMs; the parts' fp32
+// sums meet in the workspace and the pair that comes last adds them in order and
+// writes the result.
 // Tiles run group by group, a group's chunks in runs of eight per weight tile,
 // and are claimed from a counter in the workspace header that the last pair to
 // finish sets back to zero.  Data that crosses to the other CTA travels by
@@ -69,7 +70,7 @@ constexpr int F_W_BYTES = F_KB * F_KBLK_BYTES;        // this CTA's 128 weight r
 constexpr int F_STAGE_BYTES = 2 * F_W_BYTES;          // and up to 128 rows of the chunk
 constexpr int F_THREADS = 384;
 constexpr int F_EPI_WARP0 = 4, F_EPI_WARPS = 8;
-constexpr int F_CHUNK = 256;                          // most rows of a group in one tile
+constexpr int F_CHUNK = 256;                          // most rows of a group in one tile (swapped: Fp8Args::chunk)
 constexpr int F_RUN = 8;                              // chunks that walk a group's weight tiles together
 constexpr int F_XMAPS = 16;                           // row boxes of 8, 16, ..., 128 rows
 constexpr int F_TRING = 8;
@@ -112,10 +113,13 @@ struct Fp8Args {
   int nout;                // output columns per group
   int nk;                  // k-blocks
   int splits;              // parts that a tile's k-blocks are cut into
+  unsigned split_magic;    // floor(2^32 / splits) + 1: its high product with an index is the index / splits
+  int split_nk, split_rem; // k-blocks per part, one more in the first split_rem parts
   unsigned* split_count;   // [tiles] parts done
   float4* partial;         // [tiles][splits][2][partial_vecs][256]
   int partial_vecs;        // float4 per thread and part
   int n_o;                 // weight tiles per group
+  int chunk;               // most rows of a group in one tile: F_CHUNK, less (swapped) where there are few tiles
   int view;                // 1: the maps bring two k-blocks per load (K % 128 == 0)
   int nnb;                 // scale blocks along n
   const float *as, *sas;               // row scales, and those of the shared group's own rows
@@ -138,15 +142,16 @@ struct Fp8Tile {
   int index, part;                 // of the tile, its parts together; which of them
 };
 
-__device__ __forceinline__ int f8_chunks(int m) { return (m + F_CHUNK - 1) / F_CHUNK; }
+// (chunk is a power of two)
+__device__ __forceinline__ int f8_chunks(int m, int chunk) { return (m + chunk - 1) >> (31 - __clz(chunk)); }
 
 // One warp: prefix[g] = first tile of group g (n_o tiles per chunk).
-__device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int groups, int n_o) {
+__device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int groups, int n_o, int chunk) {
   const int lane = lane_id();
   int carry = 0;
   for (int base = 0; base < groups; base += 32) {
     const int g = base + lane;
-    const int v = g < groups ? f8_chunks(offs[g + 1] - offs[g]) * n_o : 0;
+    const int v = g < groups ? f8_chunks(offs[g + 1] - offs[g], chunk) * n_o : 0;
     int x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -159,35 +164,42 @@ __device__ __forceinline__ void f8_prefix(const int* offs, int* prefix, int grou
   if (lane == 0) prefix[groups] = carry;
 }
 
-template <bool WIDE>
-__device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, int groups, int n_o, int nk,
-                                             int splits) {
-  int part = 0;
-  if (splits > 1) {
-    part = t % splits;
-    t /= splits;
+// Swapped tiles divide integers only where a group has several chunks: a decode is on
+// the way of a call's first load.
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ Fp8Tile f8_decode(int t, const int* prefix, const int* offs, const Fp8Args& args) {
+  Fp8Tile tl;
+  tl.part = 0;
+  tl.kb0 = 0;
+  tl.nk = args.nk;
+  if constexpr (SPLIT) {  // at least two parts
+    const int index = (int)__umulhi((unsigned)t, args.split_magic);
+    tl.part = t - index * args.splits;
+    tl.kb0 = tl.part * args.split_nk + min(tl.part, args.split_rem);
+    tl.nk = args.split_nk + (tl.part < args.split_rem ? 1 : 0);
+    t = index;
   }
-  int lo = 0, hi = groups - 1;  // last g with prefix[g] <= t
+  tl.index = t;
+  int lo = 0, hi = args.groups - 1;  // last g with prefix[g] <= t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] <= t) lo = mid;
     else hi = mid - 1;
   }
   const int m = offs[lo + 1] - offs[lo];
-  const int ch = f8_chunks(m);
-  const int nc = WIDE ? F_CHUNK : ((m + ch - 1) / ch + 15) & ~15;
+  const int ch = f8_chunks(m, args.chunk);
   const int local = t - prefix[lo];
-  const int run = local / (n_o * F_RUN);
-  const int rem = local - run * n_o * F_RUN;
-  const int in_run = min(F_RUN, ch - run * F_RUN);
-  const int c = run * F_RUN + rem % in_run;
-  Fp8Tile tl;
-  tl.index = t;
-  tl.part = part;
-  tl.kb0 = splits > 1 ? nk * part / splits : 0;
-  tl.nk = splits > 1 ? nk * (part + 1) / splits - tl.kb0 : nk;
+  int c = 0, nc = WIDE ? F_CHUNK : (m + 15) & ~15;
+  tl.o = local;
+  if (WIDE || ch > 1) {
+    if (!WIDE) nc = ((m + ch - 1) / ch + 15) & ~15;
+    const int run = local / (args.n_o * F_RUN);
+    const int rem = local - run * args.n_o * F_RUN;
+    const int in_run = min(F_RUN, ch - run * F_RUN);
+    tl.o = rem / in_run;
+    c = run * F_RUN + rem - tl.o * in_run;
+  }
   tl.group = lo;
-  tl.o = rem / in_run;
   tl.row0 = offs[lo] + c * nc;
   tl.rows = max(0, min(nc, m - c * nc));
   tl.half = WIDE ? min(128, max(8, (tl.rows + 7) & ~7)) : max(8, ((tl.rows + 15) & ~15) >> 1);
@@ -576,7 +588,7 @@ __device__ __forceinline__ void f8_store_rows(uint8_t* block, const uint4 (&w)[B
   }
 }
 
-// SPLIT: tiles are cut along K into args.splits parts.
+// SPLIT: tiles (swapped) are cut along K into args.splits parts.
 template <int EPI, bool WIDE, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     gemm_fp8_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Args args) {
@@ -624,7 +636,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     for (int i = threadIdx.x; i < F_CHUNK; i += blockDim.x) amax_sh[i] = 0u;
   if (threadIdx.x == 0) abort_flag = 0;
   __syncthreads();
-  if (warp == 0) f8_prefix(offs_sh, prefix_sh, G, args.n_o);
+  if (warp == 0) f8_prefix(offs_sh, prefix_sh, G, args.n_o, args.chunk);
   if (threadIdx.x == 32) {
     for (int s = 0; s < F_STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -682,10 +694,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
     if (warp == 0) {
       // ======================= TMA producer (both CTAs) =======================
       if (lane == 0) {
-        tma_prefetch_map(&maps.w);
         int stage = 0;
         uint32_t phase = 0;
         long issued = 0;
+        tma_prefetch_map(&maps.w);
         bool ok = true;
         // The even CTA's producer claims tiles and publishes their indices (and
         // finally one past the last) to every role of both CTAs; a tile's
@@ -727,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
           ok = take(t);
         }
         while (ok && t < total_tiles) {
-          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
+          const Fp8Tile tl = f8_decode<WIDE, SPLIT>(t, prefix_sh, offs_sh, args);
           const bool sh = tl.group == args.shared_group;
           const CUtensorMap* wm = sh ? &maps.ws : &maps.w;
           const bool own_rows = sh && args.shared_a;
@@ -817,7 +829,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         uint32_t rph = 0;
         const uint64_t desc0 = sw128_desc(smem_base);
         while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-          const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
+          const Fp8Tile tl = f8_decode<WIDE, SPLIT>(t, prefix_sh, offs_sh, args);
           const uint32_t idesc = f8_idesc(256, WIDE ? 256 : 2 * tl.half);
           const uint32_t x_kblk = (uint32_t)(tl.half * F_BK) >> 4;  // in descriptor units of 16 bytes
           const int nk = tl.nk;
@@ -871,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       const int nkb = args.nk;
       bool ok = true;
       while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-        const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
+        const Fp8Tile tl = f8_decode<WIDE, SPLIT>(t, prefix_sh, offs_sh, args);
         const bool sh = tl.group == args.shared_group;
         const bool own_rows = sh && args.shared_a;
         const int nk = tl.nk;
@@ -973,10 +985,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (leader) {
           if (!f8_warp_wait<true>(&pair_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
           if (lane == 0) {
-            __threadfence();  // after the barriers: for every thread of the pair's epilogues
-            const bool last = atomicInc(args.split_count + tl.index, (unsigned)args.splits - 1u) ==
-                              (unsigned)args.splits - 1u;  // and back to zero for the next launch
-            __threadfence();
+            // after the barriers: releases, and acquires, for every thread of the pair's
+            // epilogues; the count goes back to zero for the next launch
+            unsigned count;
+            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                         : "=r"(count)
+                         : "l"(args.split_count + tl.index), "r"((unsigned)args.splits - 1u)
+                         : "memory");
+            const bool last = count == (unsigned)args.splits - 1u;
             last_sh = last;
             mbar_arrive(&done_bar);
             const uint32_t peer_done = map_to_rank(&done_bar, 1);
@@ -1010,17 +1026,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
       return 2;
     };
     while (ok && take_warp(rs, rph, t) && t < total_tiles) {
-      const Fp8Tile tl = f8_decode<WIDE>(t, prefix_sh, offs_sh, G, args.n_o, args.nk, SPLIT ? args.splits : 1);
+      const Fp8Tile tl = f8_decode<WIDE, SPLIT>(t, prefix_sh, offs_sh, args);
       if constexpr (WIDE) {
         const int r_cta = quarter * 32;                          // this warp's rows of the CTA's 128
         const int valid = tl.rows - ((int)rank * 128 + r_cta);   // ... of which this many exist
         if (valid <= 0) {
           ok = f8_pass_over(drain, tl.nk, args, &abort_flag);
           if (!ok) break;
-          if constexpr (SPLIT) {
-            uint64_t none[64] = {};
-            if (split_join(none, tl, 0) == 0) break;
-          }
           if constexpr (SWIGLU) ++tiles_done;  // both warps of the quarter pass the tile over
           continue;
         }
@@ -1029,11 +1041,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         for (int i = 0; i < 64; ++i) acc[i >> 3][i & 7] = 0ull;
         ok = f8_accumulate_wide<SWIGLU>(acc, drain, hf * 128, tl.nk, args, &abort_flag);
         if (!ok) break;
-        if constexpr (SPLIT) {
-          const int done = split_join(reinterpret_cast<uint64_t(&)[64]>(acc), tl, 32);
-          if (done == 0) break;
-          if (done == 1) continue;
-        }
         uint8_t* stage = smem + F_STAGES * F_STAGE_BYTES + F_SLOTS * MATS * F_CHUNK * 4 +
                          (warp - F_EPI_WARP0) * F_OUT_WIDE_BYTES;
         const size_t row = (size_t)tl.row0 + (int)rank * 128 + r_cta;
@@ -1380,11 +1387,9 @@ static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args
 template <int EPI>
 static moe_status launch_f8(bool wide, const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound,
                             cudaStream_t s) {
-  if (args.splits > 1)
-    return wide ? launch_f8_t<EPI, true, true>(maps, args, tile_bound, s)
-                : launch_f8_t<EPI, false, true>(maps, args, tile_bound, s);
-  return wide ? launch_f8_t<EPI, true, false>(maps, args, tile_bound, s)
-              : launch_f8_t<EPI, false, false>(maps, args, tile_bound, s);
+  if (wide) return launch_f8_t<EPI, true, false>(maps, args, tile_bound, s);
+  return args.splits > 1 ? launch_f8_t<EPI, false, true>(maps, args, tile_bound, s)
+                         : launch_f8_t<EPI, false, false>(maps, args, tile_bound, s);
 }
 
 // Weight map of one set of matrices; *up_first: the second lies lower in memory.
@@ -1399,46 +1404,69 @@ static moe_status weight_map(CUtensorMap* m, int epi, const Fp8Operand& b, const
   return interleaved_map(m, low, apart, rows, k, view) ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Wide tiles or swapped ones, weight tiles per group, and the most tiles there can be.
+// Wide tiles or swapped ones, most rows of a chunk, weight tiles per group, the most
+// tiles there can be, and parts that each is cut into along K.
 struct Fp8Shape {
   bool wide;
-  int n_o;
+  int chunk, n_o;
   int64_t tiles;
+  int splits;
 };
-static Fp8Shape f8_shape(bool swiglu, int64_t rows, int groups, bool offsets, int nout) {
+
+// More tiles than SM pairs: the tiling by rows per group (F_WIDE_ROWS), chunks of 256
+// rows.  With fewer, a call lasts as long as one tile, so the tile is made shorter,
+// by smaller chunks (the weights are then read more often, from L2) or by cutting it
+// along K, whichever costs least in hundredths of a microsecond, as measured on B200
+// with calls of 1 to 1000 rows, K = 1040 to 7168:
+//   a k-block       42 wide, 26 + r^2 / 2400 swapped with r rows (27, 28, 33 and 53
+//                   with 32, 64, 128 and 256): the rounds of barriers between MMA and
+//                   epilogue below 100 rows, the accumulator reads above;
+//   joining p parts 300 + 6 r + 25 p (wide tiles are not cut: smaller chunks always win).
+// 200 x 2048 x 7168 takes 23.1 us in chunks of 32 rows, 32.5 as 8 parts of whole
+// tiles; 1 x 4096 x 7168 15.9 us in 4 parts, 22.0 uncut.
+static Fp8Shape f8_shape(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k) {
   Fp8Shape f;
   f.wide = rows >= (int64_t)moe::F_WIDE_ROWS * groups;
+  f.chunk = moe::F_CHUNK;
   f.n_o = swiglu ? (nout + 127) / 128 : (nout + 255) / 256;
-  f.tiles = ((rows + moe::F_CHUNK - 1) / moe::F_CHUNK + (offsets ? groups : 0)) * f.n_o;
+  f.splits = 1;
+  auto tiles = [&](int chunk) { return ((rows + chunk - 1) / chunk + (offsets ? groups : 0)) * f.n_o; };
+  f.tiles = tiles(f.chunk);
+  const int64_t pairs = sm_count() / 2, nk = q_blocks(k);
+  if (f.tiles < 1 || f.tiles > pairs) return f;
+  const int64_t per_group = (rows + groups - 1) / groups;
+  int64_t best = f.wide ? 42 * nk : INT64_MAX;
+  for (int chunk = moe::F_CHUNK; chunk >= 32 && tiles(chunk) <= pairs; chunk /= 2) {
+    const int64_t r = std::min<int64_t>(chunk, per_group), t = tiles(chunk);
+    for (int64_t parts = 1; parts <= std::min(pairs / t, nk / 2) || parts == 1; ++parts) {
+      const int64_t cost = (26 + r * r / 2400) * ((nk + parts - 1) / parts) + (parts > 1 ? 300 + 6 * r + 25 * parts : 0);
+      if (cost >= best) continue;
+      best = cost;
+      f.wide = false;
+      f.chunk = chunk;
+      f.tiles = t;
+      f.splits = (int)parts;
+    }
+  }
   return f;
 }
 
-// Parts that each tile is cut into along K when there are at most half as many
-// tiles as SM pairs: as many as keep every pair at work, but at least eight
-// k-blocks each (joining the parts costs about as much as those).
-static int f8_splits(const Fp8Shape& f, int nk) {
-  const int64_t pairs = sm_count() / 2;
-  if (f.tiles < 1 || f.tiles > pairs / 2) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(pairs / f.tiles, nk / 8));
-}
-
-// float4 of sums per thread: 128 columns (wide), or half of the chunk in 16s
+// float4 of sums per thread: half of the chunk in 16s
 static int f8_partial_vecs(const Fp8Shape& f, int64_t rows) {
-  return f.wide ? 32 : (int)((std::min<int64_t>(moe::F_CHUNK, rows) + 31) / 32 * 4);
+  return (int)((std::min<int64_t>(f.chunk, rows) + 31) / 32 * 4);
 }
 
 size_t gemm_fp8_split_bytes(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k) {
   if (rows <= 0) return 0;
-  const Fp8Shape f = f8_shape(swiglu, rows, groups, offsets, nout);
-  const int splits = f8_splits(f, q_blocks(k));
-  return splits == 1 ? 0 : (size_t)f.tiles * splits * 2 * f8_partial_vecs(f, rows) * 256 * sizeof(float4);
+  const Fp8Shape f = f8_shape(swiglu, rows, groups, offsets, nout, k);
+  return f.splits == 1 ? 0 : (size_t)f.tiles * f.splits * 2 * f8_partial_vecs(f, rows) * 256 * sizeof(float4);
 }
 
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.max_rows == 0) return MOE_OK;
   const bool swiglu = g.epi == EPI_SWIGLU;
   const int groups = g.offsets ? g.groups : 1;
-  const Fp8Shape shape = f8_shape(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout);
+  const Fp8Shape shape = f8_shape(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout, g.k);
   const bool wide = shape.wide;
   const bool view = g.k % 128 == 0;
   const bool shared = g.sb.q != nullptr && g.offsets != nullptr;
@@ -1455,13 +1483,13 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   }
   // row boxes: only those that a chunk can take (one group: its two chunk sizes)
   auto row_maps = [&](CUtensorMap* ms, const Fp8Operand& a, int64_t rows, bool one_group) -> bool {
-    const int64_t ch = (rows + moe::F_CHUNK - 1) / moe::F_CHUNK;
+    const int64_t ch = (rows + shape.chunk - 1) / shape.chunk;
     const int64_t nc = wide ? moe::F_CHUNK : ((rows + ch - 1) / ch + 15) / 16 * 16;
     auto half = [&](int64_t r) { return wide ? std::min<int64_t>(128, (r + 7) / 8 * 8) : (r + 15) / 16 * 8; };
     const int64_t first = half(std::min(nc, rows)), last = half(rows - (ch - 1) * nc);
     for (int i = 0; i < moe::F_XMAPS; ++i) {
       const int64_t box = 8 * (i + 1);
-      if (one_group ? (box == first || box == last) : box <= half(std::min<int64_t>(moe::F_CHUNK, rows)))
+      if (one_group ? (box == first || box == last) : box <= half(std::min<int64_t>(shape.chunk, rows)))
         if (!rows_map(&ms[i], a.q, rows, g.k, a.ld, (int)box, view)) return false;
     }
     return true;
@@ -1475,13 +1503,17 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   args.nout = g.nout;
   args.nk = q_blocks(g.k);
   args.n_o = shape.n_o;
+  args.chunk = shape.chunk;
   args.splits = 1;
   args.split_count = nullptr;
   args.partial = nullptr;
   args.partial_vecs = f8_partial_vecs(shape, g.max_rows);
   const size_t split_bytes = gemm_fp8_split_bytes(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout, g.k);
   if (split_bytes > 0 && split_bytes <= g.split_bytes) {
-    args.splits = f8_splits(shape, args.nk);
+    args.splits = shape.splits;
+    args.split_magic = (unsigned)((1ull << 32) / (unsigned)args.splits + 1);  // exact: there are few tiles
+    args.split_nk = args.nk / args.splits;
+    args.split_rem = args.nk % args.splits;
     args.split_count = reinterpret_cast<unsigned*>(g.hdr) + moe::kHeaderBytes / 4;
     args.partial = static_cast<float4*>(g.split_ws);
   }
