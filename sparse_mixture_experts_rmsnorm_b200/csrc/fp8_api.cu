@@ -134,6 +134,7 @@ static moe_status ffn_fp8_impl(const moe_config* c, Fp8Gemm p, Fp8Operand w_down
   p.k = d_ff;
   p.c = y;
   p.c_scale = nullptr;
+  p.follows = between == nullptr;
   return launch_gemm_fp8(p, s);
 }
 

@@ -672,6 +672,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised before either signals the other
   tc_fence_after();
+  // A launch that follows its rows' producer directly (Fp8Gemm::follows) may get this
+  // far while that kernel still runs.  From here on memory is read that it writes.
+  asm volatile("griddepcontrol.launch_dependents;\n\tgriddepcontrol.wait;" ::: "memory");
   const uint32_t tmem_base = tmem_base_sh;
   const int total_tiles = prefix_sh[G] * (SPLIT ? args.splits : 1);
 
@@ -1155,7 +1158,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int n_base = tl.o * 256 + (int)rank * 128 + quarter * 32 + (lane >> 2);
         float* C = reinterpret_cast<float*>(args.c);
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+        for (int b = 0; b < 8; ++b) {
+          if (b * 16 >= cw) break;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -1167,6 +1171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
                 if (r + 1 < valid && r + 1 < cw) C[(row0 + r + 1) * args.nout + n] = f.y;
               }
             }
+        }
       } else if constexpr (EPI == moe_host::EPI_STORE) {
         // 16 rows x 32 columns at a time through this warp's block of shared memory
         uint8_t* stage = smem + F_STAGES * F_STAGE_BYTES + F_SLOTS * MATS * F_CHUNK * 4 +
@@ -1178,7 +1183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
           const int r0 = b * 16;
-          if (r0 >= left) continue;
+          if (r0 >= left) break;
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
@@ -1214,25 +1219,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         // the activation in place: acc[..][0] holds its pair of rows
         float m[32];
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
+        for (int i = 0; i < 32; ++i) m[i] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          if (b * 16 >= cw) break;  // (one jump: unrolled batches are long, and few rows find them cold)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float mx = 0.f, my = 0.f;
-            if (b * 16 < cw) {
 #pragma unroll
-              for (int l16 = 0; l16 < 2; ++l16) {
-                const float2 p = unpack64(acc[b][l16][j][0]), q = unpack64(acc[b][l16][j][1]);
-                const bool in = unit0 + l16 * 8 + (lane >> 2) < args.nout;
-                const float vx = in ? f8_silu_mul(up_first ? q.x : p.x, up_first ? p.x : q.x) : 0.f;
-                const float vy = in ? f8_silu_mul(up_first ? q.y : p.y, up_first ? p.y : q.y) : 0.f;
-                mx = fmaxf(mx, fabsf(vx));
-                my = fmaxf(my, fabsf(vy));
-                acc[b][l16][j][0] = pack64(__float_as_uint(vx), __float_as_uint(vy));
-              }
+            for (int l16 = 0; l16 < 2; ++l16) {
+              const float2 p = unpack64(acc[b][l16][j][0]), q = unpack64(acc[b][l16][j][1]);
+              const bool in = unit0 + l16 * 8 + (lane >> 2) < args.nout;
+              const float vx = in ? f8_silu_mul(up_first ? q.x : p.x, up_first ? p.x : q.x) : 0.f;
+              const float vy = in ? f8_silu_mul(up_first ? q.y : p.y, up_first ? p.y : q.y) : 0.f;
+              mx = fmaxf(mx, fabsf(vx));
+              my = fmaxf(my, fabsf(vy));
+              acc[b][l16][j][0] = pack64(__float_as_uint(vx), __float_as_uint(vy));
             }
             m[b * 4 + j * 2] = mx;
             m[b * 4 + j * 2 + 1] = my;
           }
+        }
         // each row's largest magnitude over the 8 lanes that share its column: a
         // reduce-scatter, after which a lane holds 4 of the 32 rows
 #pragma unroll
@@ -1281,7 +1288,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int left = min(valid, cw);
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-          if (b * 16 >= cw) continue;
+          if (b * 16 >= cw) break;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float2 inv = *reinterpret_cast<const float2*>(inv_sh + hf * 128 + b * 16 + (lane & 3) * 4 + j * 2);
@@ -1375,21 +1382,32 @@ static int f8_resident_pairs() {
 }
 
 template <int EPI, bool WIDE, bool SPLIT>
-static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound, cudaStream_t s) {
+static moe_status launch_f8_t(const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound, bool follows,
+                              cudaStream_t s) {
   static SmemLimit lim;
   const moe_status st = ensure_smem_limit(moe::gemm_fp8_kernel<EPI, WIDE, SPLIT>, moe::f8_smem_bytes<EPI, WIDE>(), lim);
   if (st != MOE_OK) return st;
   const int64_t pairs = std::min<int64_t>(tile_bound, f8_resident_pairs<EPI, WIDE, SPLIT>());
-  moe::gemm_fp8_kernel<EPI, WIDE, SPLIT><<<(unsigned)(2 * pairs), moe::F_THREADS, moe::f8_smem_bytes<EPI, WIDE>(), s>>>(maps, args);
+  cudaLaunchAttribute overlap = {};
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(moe::F_THREADS);
+  cfg.dynamicSmemBytes = moe::f8_smem_bytes<EPI, WIDE>();
+  cfg.stream = s;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = follows ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, moe::gemm_fp8_kernel<EPI, WIDE, SPLIT>, maps, args);
   return launch_status();
 }
 
 template <int EPI>
 static moe_status launch_f8(bool wide, const moe::Fp8Maps& maps, const moe::Fp8Args& args, int64_t tile_bound,
-                            cudaStream_t s) {
-  if (wide) return launch_f8_t<EPI, true, false>(maps, args, tile_bound, s);
-  return args.splits > 1 ? launch_f8_t<EPI, false, true>(maps, args, tile_bound, s)
-                         : launch_f8_t<EPI, false, false>(maps, args, tile_bound, s);
+                            bool follows, cudaStream_t s) {
+  if (wide) return launch_f8_t<EPI, true, false>(maps, args, tile_bound, follows, s);
+  return args.splits > 1 ? launch_f8_t<EPI, false, true>(maps, args, tile_bound, follows, s)
+                         : launch_f8_t<EPI, false, false>(maps, args, tile_bound, follows, s);
 }
 
 // Weight map of one set of matrices; *up_first: the second lies lower in memory.
@@ -1533,9 +1551,9 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   args.hdr = g.hdr;
   args.wait_ns = wait_limit_ns();
   const int64_t bound = shape.tiles * args.splits;  // the exact count lives on the device
-  if (swiglu) return launch_f8<EPI_SWIGLU>(wide, maps, args, bound, s);
-  if (g.epi == EPI_F32) return launch_f8<EPI_F32>(wide, maps, args, bound, s);
-  return launch_f8<EPI_STORE>(wide, maps, args, bound, s);
+  if (swiglu) return launch_f8<EPI_SWIGLU>(wide, maps, args, bound, g.follows, s);
+  if (g.epi == EPI_F32) return launch_f8<EPI_F32>(wide, maps, args, bound, g.follows, s);
+  return launch_f8<EPI_STORE>(wide, maps, args, bound, g.follows, s);
 }
 
 }  // namespace moe_host

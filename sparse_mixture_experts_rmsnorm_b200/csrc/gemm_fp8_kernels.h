@@ -30,6 +30,7 @@ struct Fp8Gemm {
   int groups = 1, max_rows = 0, nout = 0, k = 0;
   void* c = nullptr;         // [max_rows][nout]
   float* c_scale = nullptr;  // EPI_SWIGLU: [max_rows][ceil(nout / 128)]
+  bool follows = false;      // the launch before it on the stream is the product that makes a: its end may overlap
   int32_t* hdr = nullptr;    // workspace header and, behind it, the counters of cut tiles (kFp8HeaderBytes)
   void* split_ws = nullptr;  // partial sums of cut tiles
   size_t split_bytes = 0;
