@@ -126,8 +126,9 @@ const char* moe_version(void);
  * act and y_perm then hold R + N rows and there is no separate y_shared. */
 size_t moe_workspace_size(const moe_config* cfg);
 
-/* Zero the workspace header (the device error word).  Call once after
- * allocating a workspace, before its first use. */
+/* Zero the start of the workspace, up to 1 KiB (the device error word, and the
+ * counters of the 8-bit products).  Call once after allocating a workspace,
+ * before its first use. */
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Steps a1-a3: RMSNorm, router and top-k selection.
@@ -366,8 +367,11 @@ size_t moe_workspace_size_fp8(const moe_config* cfg);
  *   hidden units as moe_quantize_fp8 does, and y = t . w_down[g],
  * every product as in moe_gemm_fp8.  Groups, offsets and rows as there;
  * x [max_rows][d] e4m3, its rows ldx >= d bytes apart (ldx % 16 == 0), with
- * x_scale [max_rows][ceil(d/128)], y [max_rows][d] in the act dtype.  d % 16 == 0, d_ff % 16 == 0.  The e4m3 activation is kept
- * in the workspace (moe_workspace_size_fp8 of a config with N*k >= max_rows). */
+ * x_scale [max_rows][ceil(d/128)], y [max_rows][d] in the act dtype.
+ * d % 16 == 0, d_ff % 16 == 0.  w_gate and w_up are read through one view, so
+ * they must be two places, less than 2^40 bytes apart (MOE_ERR_UNSUPPORTED).
+ * The e4m3 activation is kept in the workspace (moe_workspace_size_fp8 of a
+ * config with N*k >= max_rows). */
 moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int32_t* offsets, int32_t max_rows,
                               const void* x, int64_t ldx, const float* x_scale, const void* w_gate,
                               const float* w_gate_scale, const void* w_up, const float* w_up_scale,
@@ -382,7 +386,8 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
  * moe_layer_forward (the router reads xn in the act dtype); the experts are
  * moe_expert_ffn_fp8.
  *   residual [N][d] or NULL (s = h); out [N][d] (may equal h or residual)
- *   d, H and Hs multiples of 16; the rest as in moe_layer_forward. */
+ *   d, H and Hs multiples of 16, each pair of gate and up matrices as in
+ *   moe_expert_ffn_fp8; the rest as in moe_layer_forward. */
 moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* weights, const void* h,
                                  const void* residual, const float* bias, void* out, const moe_routing* routing,
                                  const moe_trace* trace, void* ws, size_t ws_bytes, void* stream);

@@ -104,6 +104,12 @@ static inline bool misaligned(std::initializer_list<const void*> ps) {
   return at % 16 != 0;
 }
 
+// Gate and up lie at the two ends of one tensor-map stride, which has 40 bits.
+static inline bool one_view(const void* gate, const void* up) {
+  const uintptr_t a = (uintptr_t)gate, b = (uintptr_t)up;
+  return a != b && (a < b ? b - a : a - b) < (uintptr_t)1 << 40;
+}
+
 // The SwiGLU experts over prepared products: gate/up (activation quantised in
 // the epilogue), then down.  p carries the groups and the rows; w2 and its
 // shared form the down projection's weights.
@@ -229,7 +235,7 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
   if (!x || !x_scale || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !w_down || !w_down_scale || !y)
     return MOE_ERR_INVALID_ARG;
   if (ldx < cfg->d_model) return MOE_ERR_INVALID_ARG;
-  if (ldx % 16 || misaligned({x, w_gate, w_up, w_down})) return MOE_ERR_UNSUPPORTED;
+  if (ldx % 16 || misaligned({x, w_gate, w_up, w_down}) || !one_view(w_gate, w_up)) return MOE_ERR_UNSUPPORTED;
   Fp8Gemm p;
   p.a = operand(x, x_scale, ldx);
   p.b = operand(w_gate, w_gate_scale);
@@ -257,6 +263,7 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
       return MOE_ERR_INVALID_ARG;
     if (misaligned({w->w_gate, w->w_up, w->w_down}) || (shared && misaligned({w->ws_gate, w->ws_up, w->ws_down})))
       return MOE_ERR_UNSUPPORTED;
+    if (!one_view(w->w_gate, w->w_up) || (shared && !one_view(w->ws_gate, w->ws_up))) return MOE_ERR_UNSUPPORTED;
     if ((int64_t)E * H > 0x7fffffffLL || (int64_t)E * d > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   }
   cudaStream_t s = (cudaStream_t)stream;

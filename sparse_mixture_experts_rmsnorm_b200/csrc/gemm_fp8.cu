@@ -1417,8 +1417,7 @@ static moe_status weight_map(CUtensorMap* m, int epi, const Fp8Operand& b, const
   if (epi != EPI_SWIGLU) return rows_map(m, b.q, rows, k, k, 128, view) ? MOE_OK : MOE_ERR_CUDA;
   *up_first = b2.q < b.q;
   const uint8_t* low = *up_first ? b2.q : b.q;
-  const int64_t apart = *up_first ? b.q - b2.q : b2.q - b.q;
-  if (apart == 0 || apart >= (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;  // a TMA stride has 40 bits
+  const int64_t apart = *up_first ? b.q - b2.q : b2.q - b.q;  // not 0, and below 2^40
   return interleaved_map(m, low, apart, rows, k, view) ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -125,6 +125,27 @@ def test_layer_refusals():
                                      None) == BAD
 
 
+def test_gate_and_up_must_be_two_places_within_reach():
+    """Gate and up are one view with their distance as a stride of at most 40 bits."""
+    def ffn(gate, up):
+        return lib.moe_expert_ffn_fp8(ctypes.byref(_cfg().c()), 1, None, 64, 256, 256, 256, gate, 256, up, 256, 256,
+                                      256, 128, 256, 256, BIG, None)
+
+    def layer(gate, up, s_gate, s_up):
+        w = moe.MoeWeightsFp8()
+        for n, _ in moe.MoeWeightsFp8._fields_:
+            setattr(w, n, 256)
+        w.w_gate, w.w_up, w.ws_gate, w.ws_up = gate, up, s_gate, s_up
+        return lib.moe_layer_forward_fp8(ctypes.byref(_cfg(d_ff_shared=64).c()), ctypes.byref(w), 256, None, None, 256,
+                                         None, None, 256, BIG, None)
+
+    assert ffn(4096, 4096) == UNSUPPORTED
+    assert ffn(4096, 4096 + (1 << 40)) == UNSUPPORTED and ffn(4096 + (1 << 40), 4096) == UNSUPPORTED
+    assert layer(4096, 4096, 4096, 8192) == UNSUPPORTED
+    assert layer(4096, 8192, 4096, 4096) == UNSUPPORTED
+    assert layer(4096, 8192, 4096, 4096 + (1 << 40)) == UNSUPPORTED
+
+
 def test_python_wrapper_refuses_strided_tensors():
     import torch
     x = torch.zeros(4, 64)[:, ::2]
