@@ -145,6 +145,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _stream_of(stream, *tensors):
+    """The stream's handle, once every tensor (or None, or raw pointer) is seen to be on the current CUDA device."""
+    import torch
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != device:
+            raise ValueError("tensors passed to the MoE library must be on the current CUDA device")
+    # (the same handle as current_stream(), without making a Stream object of it)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def _torch_stream(stream):
     import torch
     if stream is None:
@@ -311,13 +322,14 @@ def moe_add_rmsnorm(cfg: Config, x, residual, norm_w, res_out, xn, q, q_scale, s
     """s = x + residual (residual may be None); res_out = s, xn = RMSNorm(s) * norm_w and (q, q_scale) = xn in e4m3
     with a scale per 128 columns; each output may be None."""
     _check(_lib.moe_add_rmsnorm(ctypes.byref(cfg.c()), _ptr(x), _ptr(residual), _ptr(norm_w), _ptr(res_out), _ptr(xn),
-                                _ptr(q), _ptr(q_scale), _stream(stream)), "moe_add_rmsnorm")
+                                _ptr(q), _ptr(q_scale),
+                                _stream_of(stream, x, residual, norm_w, res_out, xn, q, q_scale)), "moe_add_rmsnorm")
 
 
 def moe_quantize_fp8(dtype: str, block_rows: int, n_mats: int, rows: int, cols: int, x, q, scale, stream=None):
     """n_mats matrices [rows][cols] ("bf16" or "f32") to e4m3 in blocks of block_rows (1 or 128) x 128."""
     _check(_lib.moe_quantize_fp8(_DTYPES[dtype], block_rows, n_mats, rows, cols, _ptr(x), _ptr(q), _ptr(scale),
-                                 _stream(stream)), "moe_quantize_fp8")
+                                 _stream_of(stream, x, q, scale)), "moe_quantize_fp8")
 
 
 def _rows(t, cols: int):
@@ -337,8 +349,8 @@ def moe_gemm_fp8(n_groups: int, offsets, max_rows: int, n_out: int, k: int, a, a
     The rows of a may lie apart (a slice of a wider buffer)."""
     a_ptr, lda = _rows(a, k)
     _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, a_ptr, lda, _ptr(a_scale), _ptr(b),
-                             _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_gemm_fp8")
+                             _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(),
+                             _stream_of(stream, offsets, a, a_scale, b, b_scale, c, ws)), "moe_gemm_fp8")
 
 
 def moe_expert_ffn_fp8(cfg: Config, n_groups: int, offsets, max_rows: int, x, x_scale, w_gate, w_gate_scale, w_up,
@@ -347,8 +359,9 @@ def moe_expert_ffn_fp8(cfg: Config, n_groups: int, offsets, max_rows: int, x, x_
     x_ptr, ldx = _rows(x, cfg.d_model)
     _check(_lib.moe_expert_ffn_fp8(ctypes.byref(cfg.c()), n_groups, _ptr(offsets), max_rows, x_ptr, ldx, _ptr(x_scale),
                                    _ptr(w_gate), _ptr(w_gate_scale), _ptr(w_up), _ptr(w_up_scale), _ptr(w_down),
-                                   _ptr(w_down_scale), d_ff, _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_expert_ffn_fp8")
+                                   _ptr(w_down_scale), d_ff, _ptr(y), _ptr(ws), ws.numel(),
+                                   _stream_of(stream, offsets, x, x_scale, w_gate, w_gate_scale, w_up, w_up_scale,
+                                              w_down, w_down_scale, y, ws)), "moe_expert_ffn_fp8")
 
 
 def moe_layer_forward_fp8(cfg: Config, weights: dict, h, residual, bias, out, ws, routing: dict | None = None,
@@ -361,7 +374,9 @@ def moe_layer_forward_fp8(cfg: Config, weights: dict, h, residual, bias, out, ws
     _check(_lib.moe_layer_forward_fp8(ctypes.byref(cfg.c()), ctypes.byref(w), _ptr(h), _ptr(residual), _ptr(bias),
                                       _ptr(out), ctypes.byref(r) if r is not None else None,
                                       ctypes.byref(tr) if tr is not None else None,
-                                      _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward_fp8")
+                                      _ptr(ws), ws.numel(),
+                                      _stream_of(stream, *weights.values(), h, residual, bias, out, ws)),
+           "moe_layer_forward_fp8")
 
 
 def moe_check_device_error(ws, stream=None):

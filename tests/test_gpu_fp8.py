@@ -467,6 +467,22 @@ def test_layer_matches_the_bf16_layer(env):
     assert float((a - b).norm() / a.norm()) <= 0.1
 
 
+def test_tensors_off_the_current_device_are_refused(env):
+    """On the host, before anything is launched."""
+    torch, moe = env
+    cfg = moe.Config(4, 128, 1, 1, 16)
+    x, w, out = torch.ones(4, 128), torch.ones(128), torch.ones(4, 128, device="cuda")
+    with pytest.raises(ValueError):
+        moe.moe_add_rmsnorm(cfg, x.bfloat16(), None, w.bfloat16().cuda(), out.bfloat16(), None, None, None)
+    with pytest.raises(ValueError):
+        moe.moe_quantize_fp8("f32", 1, 1, 4, 128, out, torch.empty(4, 128, dtype=torch.uint8), torch.empty(4, 1).cuda())
+    ws = moe.workspace_gemm_fp8(1, 4, 128, 128)
+    q, s = torch.zeros(4, 128, dtype=torch.uint8, device="cuda"), torch.ones(4, 1, device="cuda")
+    b, bs = torch.zeros(128, 128, dtype=torch.uint8, device="cuda"), torch.ones(1, 1)
+    with pytest.raises(ValueError):
+        moe.moe_gemm_fp8(1, None, 4, 128, 128, q, s, b, bs, "f32", out, ws)
+
+
 # ---------------------------------------------------------------- streams, graphs, guard bands
 def test_graph_capture_and_other_stream(env):
     torch, moe = env
