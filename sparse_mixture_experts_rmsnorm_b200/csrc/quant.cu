@@ -8,6 +8,7 @@
 //   v  = fl32(fl32(s * r) * w),  xn = act(v),  (q, q_scale) from v per 128 columns.
 // xn has the bits that moe_route gives for h = s.
 #include <algorithm>
+#include <type_traits>
 
 #include "gemm_fp8_kernels.h"
 #include "quant_common.cuh"
@@ -61,18 +62,23 @@ __device__ __forceinline__ float lanes_max(float m) {
   return m;
 }
 
-// Many rows: one block of up to 256 threads per row (grid-stride), the row s staged
+// Many rows: one block per row (grid-stride), the row s staged
 // in shared memory in its own type; every warp takes whole blocks of 128 columns
 // in the second pass, so a scale needs no shared memory.  Bound by HBM; few
 // registers keep many rows in flight: 8192 rows of 7168 bf16 columns with residual
-// and every output move at 5.7 TB/s, the register form below at 4.9 at most.
-template <typename T, int V>
-__global__ void __launch_bounds__(256) add_rmsnorm_staged_kernel(const T* x, const T* residual, const T* __restrict__ w,
+// and every output move at 5.4 to 5.8 TB/s, the register form below at 4.9 at most.
+// SHIFTED (V = 1): rows of odd widths start anywhere, so the first pass takes the
+// aligned 16-byte pieces between a row's ends, at the same place of a piece in shared
+// memory; x, residual and res_out start alike.  With residual and every output, 2048
+// rows of 5003 fp32 columns take 41 us (63 by single elements), 8192 of 1027 bf16 33
+// (54).
+template <typename T, int V, bool SHIFTED, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS) add_rmsnorm_staged_kernel(const T* x, const T* residual, const T* __restrict__ w,
                                                           T* res_out, T* xn, uint8_t* __restrict__ q,
                                                           float* __restrict__ q_scale, int n, int d, float eps) {
   extern __shared__ __align__(16) uint8_t row_raw[];
   T* row = reinterpret_cast<T*>(row_raw);
-  __shared__ double part[8];
+  __shared__ double part[32];
   __shared__ float r_sh;
   constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses;
   const int warps = blockDim.x >> 5;
@@ -80,20 +86,39 @@ __global__ void __launch_bounds__(256) add_rmsnorm_staged_kernel(const T* x, con
   for (int t = blockIdx.x; t < n; t += gridDim.x) {
     const size_t base = (size_t)t * d;
     double acc = 0.0;
-    for (int i = threadIdx.x * V; i < d; i += blockDim.x * V) {
-      Pack<T, V> s = load_pack<T, V>(x + base + i);
+    // N elements from element at of the row, kept in shared memory from `to`
+    auto first_pass = [&](auto count, int at, T* to) {
+      constexpr int N = decltype(count)::value;
+      Pack<T, N> s = load_pack<T, N>(x + base + at);
       if (residual != nullptr) {
-        const Pack<T, V> b = load_pack<T, V>(residual + base + i);
+        const Pack<T, N> b = load_pack<T, N>(residual + base + at);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s.v[j] = from_f32<T>(__fadd_rn(to_f32(s.v[j]), to_f32(b.v[j])));
+        for (int j = 0; j < N; ++j) s.v[j] = from_f32<T>(__fadd_rn(to_f32(s.v[j]), to_f32(b.v[j])));
       }
-      if (res_out != nullptr) store_pack<T, V>(res_out + base + i, s);
-      store_pack<T, V>(row + i, s);
+      if (res_out != nullptr) store_pack<T, N>(res_out + base + at, s);
+      store_pack<T, N>(to, s);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
+      for (int j = 0; j < N; ++j) {
         const double f = (double)to_f32(s.v[j]);
         acc += f * f;
       }
+    };
+    const T* kept = row;
+    if constexpr (SHIFTED) {
+      constexpr int P = 16 / (int)sizeof(T);
+      const int shift = (int)((uintptr_t)(x + base) % 16 / sizeof(T)), end = shift + d;
+      kept = row + shift;
+      for (int i = threadIdx.x * P; i < end; i += blockDim.x * P) {
+        if (i >= shift && i + P <= end) {
+          first_pass(std::integral_constant<int, P>(), i - shift, row + i);
+        } else {
+          for (int j = max(i, shift); j < min(i + P, end); ++j)
+            first_pass(std::integral_constant<int, 1>(), j - shift, row + j);
+        }
+      }
+    } else {
+      for (int i = threadIdx.x * V; i < d; i += blockDim.x * V)
+        first_pass(std::integral_constant<int, V>(), i, row + i);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
@@ -117,7 +142,7 @@ __global__ void __launch_bounds__(256) add_rmsnorm_staged_kernel(const T* x, con
       for (int p = 0; p < PASSES; ++p) {
         const int c = b * Q_BLOCK + (p * LANES + lane) * V;
         if (c < d) {
-          const Pack<T, V> s = load_pack<T, V>(row + c), wv = load_pack<T, V>(w + c);
+          const Pack<T, V> s = load_pack<T, V>(kept + c), wv = load_pack<T, V>(w + c);
           Pack<T, V> o;
 #pragma unroll
           for (int j = 0; j < V; ++j) {
@@ -145,9 +170,8 @@ __global__ void __launch_bounds__(256) add_rmsnorm_staged_kernel(const T* x, con
 // One block per row (grid-stride), the row in registers: LANES lanes hold NBW
 // blocks of 128 columns, UNITS apart, so that every sum and every block's largest
 // magnitude is a few shuffles away.  For few rows (NBW = 1 spreads a row of up to
-// 1024 LANES lanes over one block: latency) and for odd widths (V = 1), where it has
-// more loads in flight than the staged form: 2048 rows of 5003 fp32 columns, 37
-// against 45 us.
+// 1024 LANES lanes over one block: latency) and for rows that start unaligned in
+// different ways (V = 1).
 template <typename T, int V, int NBW>
 __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* residual, const T* __restrict__ w,
                                                            T* res_out, T* xn, uint8_t* __restrict__ q,
@@ -374,20 +398,36 @@ static moe_status add_rmsnorm_t(const void* x, const void* residual, const void*
 #define MOE_ADD_RMSNORM(NBW)                                                                                   \
   moe::add_rmsnorm_kernel<T, V, NBW><<<grid, threads(NBW), 0, s>>>((const T*)x, (const T*)residual, (const T*)w, \
                                                                    (T*)res_out, (T*)xn, q, q_scale, n, d, eps)
+  // unaligned rows that start alike in x, residual and res_out
+  auto alike = [&](const void* p) { return p == nullptr || ((uintptr_t)p - (uintptr_t)x) % 16 == 0; };
+  const bool shifted = V == 1 && alike(residual) && alike(res_out) && (uintptr_t)x % sizeof(T) == 0;
   if (few) {
     MOE_ADD_RMSNORM(1);
-  } else if constexpr (V == 1) {
-    if (threads(4) <= 1024) MOE_ADD_RMSNORM(4);
-    else MOE_ADD_RMSNORM(12);  // d up to 49152
+  } else if (V == 1 && !shifted) {
+    if constexpr (V == 1) {
+      if (threads(4) <= 1024) MOE_ADD_RMSNORM(4);
+      else MOE_ADD_RMSNORM(12);  // d up to 49152
+    }
   } else {
-    static SmemLimit lim;
-    const int smem = (int)((size_t)d * sizeof(T));
-    const moe_status st = ensure_smem_limit(moe::add_rmsnorm_staged_kernel<T, V>, smem, lim);
+    constexpr int P = 16 / (int)sizeof(T);
+    const int smem = (int)((size_t)(d + (V == 1 ? P : 0)) * sizeof(T));
+    const int blocks = std::max(1, 220 * 1024 / smem);  // that an SM holds
+    auto launch = [&](auto kernel, SmemLimit& lim, int threads) -> moe_status {
+      const moe_status st = ensure_smem_limit(kernel, smem, lim);
+      if (st != MOE_OK) return st;
+      kernel<<<grid, threads, smem, s>>>((const T*)x, (const T*)residual, (const T*)w, (T*)res_out, (T*)xn, q, q_scale,
+                                         n, d, eps);
+      return MOE_OK;
+    };
+    static SmemLimit lim_short, lim_long;
+    // Short rows: about four passes over the row by 64 to 192 threads.  Long ones, of
+    // which an SM holds few: 1024 threads an SM (512 rows of 40001 fp32 columns with
+    // residual 94 us, 289 with 192 threads; 1024 of 16384 80 and 97).
+    const moe_status st =
+        blocks > 4 ? launch(moe::add_rmsnorm_staged_kernel<T, V, V == 1, 256>, lim_short,
+                            std::min(192, std::max(64, (d / P + 127) / 128 * 32)))
+                   : launch(moe::add_rmsnorm_staged_kernel<T, V, V == 1, 1024>, lim_long, 1024 / blocks / 32 * 32);
     if (st != MOE_OK) return st;
-    // about four passes over the row, 64 to 192 threads
-    const int t = std::min(192, std::max(64, (d / V + 127) / 128 * 32));
-    moe::add_rmsnorm_staged_kernel<T, V><<<grid, t, smem, s>>>((const T*)x, (const T*)residual, (const T*)w,
-                                                               (T*)res_out, (T*)xn, q, q_scale, n, d, eps);
   }
 #undef MOE_ADD_RMSNORM
   return launch_status();

@@ -72,6 +72,36 @@ def test_add_rmsnorm(env, dtype, n, d, residual):
     assert torch.equal(x3, xn)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [(1, 1, 1, 0), (3, 3, 3, 2), (1, 2, 1, 0), (0, 0, 5, 1)])
+@pytest.mark.parametrize("n,d", [(300, 1001), (297, 7), (300, 1024), (300, 30001)])
+def test_norm_of_tensors_that_start_unaligned(env, dtype, at, n, d):
+    """x, residual, res_out and xn start `at` elements past a 16-byte boundary, alike or not; nothing around res_out
+    and xn is written."""
+    torch, moe = env
+    t = _type(torch, dtype)
+
+    def place(shift, fill=None):
+        whole = torch.full((n * d + 64,), 7.0, dtype=t, device="cuda")
+        view = whole[8 + shift:8 + shift + n * d].view(n, d)
+        if fill is not None:
+            view.copy_(fill)
+        return whole, view
+
+    x, r = place(at[0], torch.randn(n, d, device="cuda"))[1], place(at[1], torch.randn(n, d, device="cuda"))[1]
+    (res_all, res), (xn_all, xn) = place(at[2]), place(at[3])
+    w = (1 + 0.1 * torch.randn(d, device="cuda")).to(t)
+    q, s = torch.empty(n, d, dtype=f8.E4M3, device="cuda"), torch.empty(n, f8.blocks(d), device="cuda")
+    moe.moe_add_rmsnorm(moe.Config(n, d, 1, 1, 16, dtype=dtype), x, r, w, res, xn, q, s)
+    assert torch.equal(res, (x.float() + r.float()).to(t))
+    h = res.double()
+    v = h / torch.sqrt(h.square().mean(1, keepdim=True) + 1e-6) * w.double()
+    _close(xn, v, v.abs() * 3 * U32, dtype)
+    f8.check_quantized(q, s, v, 1)
+    for whole, shift in ((res_all, at[2]), (xn_all, at[3])):
+        assert torch.all(whole[:8 + shift] == 7.0) and torch.all(whole[8 + shift + n * d:] == 7.0)
+
+
 def test_norm_bits_are_those_of_route(env):
     """xn of the fused norm equals moe_route's for h = x + residual."""
     torch, moe = env
