@@ -265,18 +265,34 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const T* x, const T* 
   }
 }
 
-template <bool WHOLE>
-constexpr int kUnroll = WHOLE ? 4 : 2;
+// The largest magnitude of a pack, NaN aside; bf16 pairs are compared as they are.
+template <typename T, int V>
+__device__ __forceinline__ float pack_amax(const Pack<T, V>& x) {
+  if constexpr (sizeof(T) == 2 && V == 8) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
+    __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(x.v[j])));
+    return m;
+  }
+}
 
-// 1 x 128 blocks: LANES lanes take one block of one row, UNROLL of them in flight;
-// a thread block takes consecutive ones (4096 x 14336 bf16: 35 us, 5.0 TB/s; with its
-// blocks a grid's width apart 43 us).
+// Blocks of 128 columns that LANES lanes of the row quantisation take at once.
+constexpr int Q_UNROLL = 2;
+
+// 1 x 128 blocks: LANES lanes take UNROLL blocks of a row; a thread block takes
+// consecutive ones.  A block's two divisions cost as much as its codes when every lane
+// does them, so the lanes share the blocks' maxima out (4096 x 14336 bf16: 31 us,
+// 5.7 TB/s; all lanes for each block 35.5 us; thread blocks a grid's width apart 43).
 // WHOLE: the columns are whole blocks, so block u is the 128 elements from 128 u
 // on and no division finds its row.
 template <typename T, int V, bool WHOLE>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
                                                             float* __restrict__ scale, int64_t units, int cols) {
-  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses, UNROLL = kUnroll<WHOLE>;
+  constexpr int LANES = BlockLanes<V>::kLanes, PASSES = BlockLanes<V>::kPasses, UNROLL = Q_UNROLL;
   const int nb = (cols + Q_BLOCK - 1) / Q_BLOCK;
   const int lane = threadIdx.x % LANES;
   const int across = blockDim.x / LANES;  // blocks of 128 columns that the thread block takes at once
@@ -300,17 +316,37 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
     for (int p = 0; p < PASSES; ++p)
       if (p * LANES * V < left[k]) s[k][p] = load_pack<T, V>(x + at[k] + p * (LANES * V));
   }
+  float m[UNROLL];
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
-    float m = 0.f;
+    m[k] = 0.f;
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
-      if (p * LANES * V < left[k]) {
+      if (p * LANES * V < left[k]) m[k] = fmaxf(m[k], pack_amax<T, V>(s[k][p]));
+  }
+  // the UNROLL maxima together: LANES / UNROLL lanes end up with one of them, whose
+  // divisions they do
+  int mine = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(s[k][p].v[j])));
+  for (int n = UNROLL / 2, o = LANES / 2; o > 0; n >>= 1, o >>= 1) {
+    if (n > 0) {
+      const bool upper = lane & o;
+      mine += upper ? n : 0;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float give = upper ? m[i] : m[i + n], keep = upper ? m[i + n] : m[i];
+        m[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
       }
-    const float sc = quant_scale(lanes_max<LANES>(m));
-    const float inv = __frcp_rn(sc);
+    } else {
+      m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], o));
+    }
+  }
+  const float my_scale = quant_scale(m[0]);
+  const float my_inv = __frcp_rn(my_scale);
+  if (lane % (LANES / UNROLL) == 0 && u0 + mine * across < units) scale[u0 + mine * across] = my_scale;
+#pragma unroll
+  for (int k = 0; k < UNROLL; ++k) {
+    const float inv = __shfl_sync(0xffffffffu, my_inv, k * (LANES / UNROLL), LANES);
 #pragma unroll
     for (int p = 0; p < PASSES; ++p)
       if (p * LANES * V < left[k]) {
@@ -319,22 +355,6 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
         for (int j = 0; j < V; ++j) v[j] = to_f32(s[k][p].v[j]);
         store_codes<V>(q + at[k] + p * (LANES * V), v, inv);
       }
-    if (lane == 0 && u0 + k * across < units) scale[u0 + k * across] = sc;
-  }
-}
-
-// The largest magnitude of a pack, NaN aside; bf16 pairs are compared as they are.
-template <typename T, int V>
-__device__ __forceinline__ float pack_amax(const Pack<T, V>& x) {
-  if constexpr (sizeof(T) == 2 && V == 8) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&x);
-    __nv_bfloat162 m = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
-    return fmaxf(__low2float(m), __high2float(m));
-  } else {
-    float m = 0.f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(to_f32(x.v[j])));
-    return m;
   }
 }
 
@@ -420,12 +440,15 @@ static moe_status add_rmsnorm_t(const void* x, const void* residual, const void*
       return MOE_OK;
     };
     static SmemLimit lim_short, lim_long;
-    // Short rows: about four passes over the row by 64 to 192 threads.  Long ones, of
-    // which an SM holds few: 1024 threads an SM (512 rows of 40001 fp32 columns with
-    // residual 94 us, 289 with 192 threads; 1024 of 16384 80 and 97).
+    // Short rows: about four passes over the row by 64 to 192 threads, up to 256 where an
+    // SM holds seven rows or fewer (4096 rows of 14336 bf16 columns with residual 94 us,
+    // 110 with 192; 8192 of 7168, where it holds 15, 91 and 105 with 256).  Long ones, of
+    // which it holds four at most: 1024 threads an SM (512 rows of 40001 fp32 columns
+    // 94 us, 289 with 192 threads; 1024 of 16384 80 and 97).
+    const int passes = std::min(192, std::max(64, (d / P + 127) / 128 * 32));
     const moe_status st =
         blocks > 4 ? launch(moe::add_rmsnorm_staged_kernel<T, V, V == 1, 256>, lim_short,
-                            std::min(192, std::max(64, (d / P + 127) / 128 * 32)))
+                            std::max(passes, std::min(256, 1792 / blocks / 32 * 32)))
                    : launch(moe::add_rmsnorm_staged_kernel<T, V, V == 1, 1024>, lim_long, 1024 / blocks / 32 * 32);
     if (st != MOE_OK) return st;
   }
@@ -453,7 +476,7 @@ static moe_status quantize_t(int block_rows, int mats, int rows, int cols, const
   if (block_rows == 1) {
     const int64_t units = (int64_t)mats * rows * nb;
     const bool whole = V > 1 && cols % moe::Q_BLOCK == 0;
-    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes * (whole ? moe::kUnroll<true> : moe::kUnroll<false>);
+    const int64_t per_block = 256 / moe::BlockLanes<V>::kLanes * moe::Q_UNROLL;
     const int64_t blocks = (units + per_block - 1) / per_block;
     if (blocks > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
     if (whole)
