@@ -358,15 +358,24 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
   }
 }
 
-// 128 x 128 blocks: 512 threads keep one tile in registers, in its own type (the
-// fp32 form of a bf16 tile would leave room for two blocks per SM only).
+// 128 x 128 blocks: a thread block keeps one tile in registers, in its own type,
+// between reading it and writing its codes; other blocks of the SM read meanwhile.
+// 16-byte bf16 accesses (V = 8): four blocks of 256 threads, 8 x 14336 x 4096 in
+// 204 us (6.9 TB/s; 5 blocks 208, 6 283, 3 217, two of 512 threads 272).  Otherwise two
+// blocks of 512, whose tiles need as many registers (8 x 7168 x 2048 fp32 103 us,
+// 5.7 TB/s; four of 256 125).
+template <int V>
+constexpr int kTileThreads = V == 8 ? 256 : 512;
+template <int V>
+constexpr int kTileBlocks = V == 8 ? 4 : 2;
 template <typename T, int V>
-__global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const T* __restrict__ x, uint8_t* __restrict__ q,
-                                                                float* __restrict__ scale, int mats, int rows,
-                                                                int cols) {
+__global__ void __launch_bounds__(kTileThreads<V>, kTileBlocks<V>)
+    quantize_tiles_kernel(const T* __restrict__ x, uint8_t* __restrict__ q, float* __restrict__ scale, int mats, int rows,
+                          int cols) {
   constexpr int ACROSS = Q_BLOCK / V;       // threads across a tile row
-  constexpr int STEP = 512 / ACROSS;        // rows per pass
-  constexpr int PASSES = Q_BLOCK / STEP;    // 4 (V = 8), 8 (V = 4) or 32 (V = 1)
+  constexpr int WARPS = kTileThreads<V> / 32;
+  constexpr int STEP = kTileThreads<V> / ACROSS;  // rows per pass
+  constexpr int PASSES = Q_BLOCK / STEP;          // 8 (V = 8, 4) or 32 (V = 1)
   __shared__ float part[2][16];
   const int rb = (rows + Q_BLOCK - 1) / Q_BLOCK, cb = gridDim.x;
   const int tr = threadIdx.x / ACROSS;
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(512, 2) quantize_tiles_kernel(const T* __restr
       m = lanes_max<32>(m);
       if (lane_id() == 0) part[parity][warp_id()] = m;
       __syncthreads();
-      m = lanes_max<16>(part[parity][lane_id() & 15]);
+      m = lanes_max<WARPS>(part[parity][lane_id() & (WARPS - 1)]);
       const float sc = quant_scale(m);
       const float inv = __frcp_rn(sc);
 #pragma unroll
@@ -486,7 +495,7 @@ static moe_status quantize_t(int block_rows, int mats, int rows, int cols, const
     return launch_status();
   }
   const dim3 grid((unsigned)nb, (unsigned)std::min(q_blocks(rows), 65535), (unsigned)std::min(mats, 65535));
-  moe::quantize_tiles_kernel<T, V><<<grid, 512, 0, s>>>((const T*)x, q, scale, mats, rows, cols);
+  moe::quantize_tiles_kernel<T, V><<<grid, moe::kTileThreads<V>, 0, s>>>((const T*)x, q, scale, mats, rows, cols);
   return launch_status();
 }
 
