@@ -337,8 +337,11 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, const void* x, const void* res
 moe_status moe_quantize_fp8(int32_t dtype, int32_t block_rows, int32_t n_mats, int32_t rows, int32_t cols,
                             const void* x, void* q, float* scale, void* stream);
 
-/* Bytes of workspace that moe_gemm_fp8 needs for these sizes; 0 if they are
- * invalid.  Initialise it once with moe_workspace_init. */
+/* Bytes of workspace that moe_gemm_fp8 uses for these sizes; 0 if they are
+ * invalid.  Initialise it once with moe_workspace_init.  Products of few tiles
+ * keep partial sums in it: a workspace sized for other sizes, of 1 KiB at
+ * least, serves too, and where the sums do not fit the call does without them
+ * (slower, and its fp32 sums are formed in another order). */
 size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n_out, int32_t k);
 
 /* Block-scaled product, grouped by expert: for the rows r in
@@ -359,7 +362,8 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
                         int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of workspace for moe_expert_ffn_fp8 and moe_layer_forward_fp8 with
- * this config; 0 if it is invalid. */
+ * this config; 0 if it is invalid.  One sized for more tokens serves fewer
+ * (room for partial sums as in moe_gemm_fp8). */
 size_t moe_workspace_size_fp8(const moe_config* cfg);
 
 /* moe_expert_ffn on e4m3 operands: per group g,

@@ -86,8 +86,16 @@ static moe_status check_fp8(const moe_config* c, const void* ws, size_t ws_bytes
   if (!config_ok(c)) return MOE_ERR_INVALID_ARG;
   if (!fp8_supported(c)) return MOE_ERR_UNSUPPORTED;
   if (ws == nullptr || ((uintptr_t)ws % 256) != 0) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < fp8_layout(c).total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < fp8_layout(c).split) return MOE_ERR_WORKSPACE;
   return MOE_OK;
+}
+
+// The layout in a workspace that may have been sized for another number of tokens:
+// the partial sums, at its end, have the room that is left.
+static Fp8Layout fp8_layout_in(const moe_config* c, size_t ws_bytes) {
+  Fp8Layout L = fp8_layout(c);
+  L.split_bytes = std::min(L.split_bytes, ws_bytes - L.split);
+  return L;
 }
 
 #define MOE_TRY(x)                 \
@@ -188,14 +196,14 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
                         const void* a, int64_t lda, const float* a_scale, const void* b, const float* b_scale,
                         int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream) {
   NvtxScope range("moe_gemm_fp8");
-  const size_t need = moe_workspace_size_gemm_fp8(n_groups, max_rows, n_out, k);
-  if (need == 0 || (offsets == nullptr && n_groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (n_groups < 1 || n_groups > moe::TC_MAX_GROUPS || max_rows < 0 || n_out < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  if (offsets == nullptr && n_groups != 1) return MOE_ERR_INVALID_ARG;
   if (c_dtype != MOE_F32 && c_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || ((uintptr_t)ws % 256) != 0) return MOE_ERR_INVALID_ARG;
   if (max_rows > 0 && (!a || !a_scale || !b || !b_scale || !c)) return MOE_ERR_INVALID_ARG;
   if (lda < k) return MOE_ERR_INVALID_ARG;
   if (k % 16 || lda % 16 || misaligned({a, b}) || (int64_t)n_groups * n_out > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
-  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < kFp8HeaderBytes) return MOE_ERR_WORKSPACE;  // (with no room for parts, no tile is cut)
   Fp8Gemm g;
   g.epi = c_dtype == MOE_BF16 ? EPI_STORE : EPI_F32;
   g.a = operand(a, a_scale, lda);
@@ -228,7 +236,7 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
   if (offsets == nullptr && n_groups != 1) return MOE_ERR_INVALID_ARG;
   if (d_ff % 16 || (int64_t)n_groups * d_ff > 0x7fffffffLL || (int64_t)n_groups * cfg->d_model > 0x7fffffffLL)
     return MOE_ERR_UNSUPPORTED;
-  const Fp8Layout L = fp8_layout(cfg);
+  const Fp8Layout L = fp8_layout_in(cfg, ws_bytes);
   if ((int64_t)max_rows * d_ff > L.act_elems || (int64_t)max_rows * q_blocks(d_ff) > L.act_scales)
     return MOE_ERR_WORKSPACE;
   if (max_rows == 0) return MOE_OK;
@@ -267,7 +275,7 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
     if ((int64_t)E * H > 0x7fffffffLL || (int64_t)E * d > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   }
   cudaStream_t s = (cudaStream_t)stream;
-  const Fp8Layout L = fp8_layout(cfg);
+  const Fp8Layout L = fp8_layout_in(cfg, ws_bytes);
   if (L.rows + N > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
   auto pick = [&](void* user, size_t off) { return user ? user : (void*)wsp(ws, off); };
   void* xn = wsp(ws, L.xn);

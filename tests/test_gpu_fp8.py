@@ -271,6 +271,21 @@ def test_few_tiles_cut_along_k(env, out, sizes, n, k):
     assert moe.moe_check_device_error(ws)[0] == 0
 
 
+def test_a_workspace_of_other_sizes_serves(env):
+    """One row with the workspace of many, and with the least there is: no room for parts, the same product."""
+    torch, moe = env
+    n, k = 512, 4096
+    aq, as_, bq, bs = _operands(torch, [1], n, k)
+    want, mag = f8.product(f8.values(aq, as_, 1), f8.values(bq, bs, 128), [1])
+    assert moe.library().moe_workspace_size_gemm_fp8(1, 1, n, k) > 4096
+    own = moe.workspace_gemm_fp8(1, 1, n, k)
+    for ws in (own, moe.workspace_gemm_fp8(1, 100000, n, k), moe.workspace_gemm_fp8(1, 1, 64, 64)):
+        c = torch.empty(1, n, device="cuda")
+        moe.moe_gemm_fp8(1, None, 1, n, k, aq, as_, bq, bs, "f32", c, ws)
+        _close(c, want, mag * U32 * (k + 32), "f32")
+        assert moe.moe_check_device_error(ws)[0] == 0
+
+
 def test_rows_that_lie_apart(env):
     """a (and the FFN's x) may be a slice of a wider buffer: the same bits as from a packed copy."""
     torch, moe = env
@@ -375,6 +390,26 @@ def test_expert_ffn(env, out, sizes, d, h):
     assert float(near.double().mean()) >= 0.9 or rows * h < 4096
     assert torch.all(y[rows:] == 7.0)
     assert moe.moe_check_device_error(ws)[0] == 0
+
+
+def test_ffn_in_a_workspace_of_more_tokens(env):
+    """Fewer tokens may want more room for partial sums than more do: the call then does without."""
+    torch, moe = env
+    d, h, rows = 4096, 2048, 32
+    small, large = moe.Config(rows, d, 1, 1, h), moe.Config(64, d, 1, 1, h)
+    size = moe.library().moe_workspace_size_fp8
+    assert size(small.c()) > size(large.c())
+    x, xs, gq, gs = _operands(torch, [rows], h, d)
+    _, _, uq, us = _operands(torch, [1], h, d)
+    _, _, dq, ds = _operands(torch, [1], d, h)
+    want, mag, flips = _ffn_want(torch, f8.values(x, xs, 1), *(f8.values(q, s, 128) for q, s in
+                                                             ((gq, gs), (uq, us), (dq, ds))), [rows])
+    for cfg in (small, large):
+        ws = moe.workspace_fp8(cfg)
+        y = torch.empty(rows, d, dtype=torch.bfloat16, device="cuda")
+        moe.moe_expert_ffn_fp8(small, 1, None, rows, x, xs, gq, gs, uq, us, dq, ds, h, y, ws)
+        _close(y, want, mag * 1e-5 + flips, "bf16")
+        assert moe.moe_check_device_error(ws)[0] == 0
 
 
 # ---------------------------------------------------------------- the operators together, as the layer uses them
