@@ -271,6 +271,33 @@ def test_few_tiles_cut_along_k(env, out, sizes, n, k):
     assert moe.moe_check_device_error(ws)[0] == 0
 
 
+def test_offsets_past_32_bits(env):
+    """Weights and results of more than 4 Gi elements: the last group's product, and the last rows."""
+    torch, moe = env
+    g, n, k = 300, 2048, 7168
+    aq, as_, bq, bs = _operands(torch, [3], n, k)
+    want, mag = f8.product(f8.values(aq, as_, 1), f8.values(bq, bs, 128), [3])
+    b = torch.zeros(g, n, k, dtype=torch.uint8, device="cuda").view(f8.E4M3)
+    scale = torch.ones(g, f8.blocks(n), f8.blocks(k), device="cuda")
+    b[-1], scale[-1] = bq[0], bs[0]
+    c = torch.empty(3, n, device="cuda")
+    offs = torch.zeros(g + 1, dtype=torch.int32, device="cuda")
+    offs[-1] = 3
+    moe.moe_gemm_fp8(g, offs, 3, n, k, aq, as_, b, scale, "f32", c, moe.workspace_gemm_fp8(g, 3, n, k))
+    _close(c, want, mag * U32 * (k + 32), "f32")
+    del b, scale
+    rows, n, k = 70000, 65536, 16
+    aq, as_, bq, bs = _operands(torch, [rows], n, k)
+    c = torch.empty(rows, n, dtype=torch.bfloat16, device="cuda")
+    moe.moe_gemm_fp8(1, None, rows, n, k, aq, as_, bq, bs, "bf16", c, moe.workspace_gemm_fp8(1, rows, n, k))
+    for r in (slice(0, 40), slice(rows - 40, rows)):
+        want, mag = f8.product(f8.values(aq[r], as_[r], 1), f8.values(bq, bs, 128), [40])
+        _close(c[r], want, mag * U32 * (k + 32), "bf16")
+    q, s = torch.empty(rows, n, dtype=torch.uint8, device="cuda").view(f8.E4M3), torch.empty(rows, n // 128, device="cuda")
+    moe.moe_quantize_fp8("bf16", 1, 1, rows, n, c, q, s)
+    f8.check_quantized(q[-40:], s[-40:], c[-40:].double(), 1)
+
+
 def test_a_workspace_of_other_sizes_serves(env):
     """One row with the workspace of many, and with the least there is: no room for parts, the same product."""
     torch, moe = env
