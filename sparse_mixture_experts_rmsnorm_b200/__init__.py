@@ -368,14 +368,15 @@ def moe_layer_forward_fp8(cfg: Config, weights: dict, h, residual, bias, out, ws
                           trace: dict | None = None, stream=None):
     """The whole layer with e4m3 experts; ``weights``: norm_w, w_router and each
     expert matrix with its ``<name>_scale``.  residual (or None) is added to h first."""
-    w = MoeWeightsFp8(*[_ptr(weights.get(n)) for n, _ in MoeWeightsFp8._fields_])
+    mats = [weights.get(n) for n, _ in MoeWeightsFp8._fields_]
+    w = MoeWeightsFp8(*[_ptr(t) for t in mats])
     r = _routing_struct(routing)
     tr = _trace_struct(trace, stream)
     _check(_lib.moe_layer_forward_fp8(ctypes.byref(cfg.c()), ctypes.byref(w), _ptr(h), _ptr(residual), _ptr(bias),
                                       _ptr(out), ctypes.byref(r) if r is not None else None,
                                       ctypes.byref(tr) if tr is not None else None,
                                       _ptr(ws), ws.numel(),
-                                      _stream_of(stream, *weights.values(), h, residual, bias, out, ws)),
+                                      _stream_of(stream, *mats, h, residual, bias, out, ws)),
            "moe_layer_forward_fp8")
 
 
