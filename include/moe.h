@@ -126,9 +126,9 @@ const char* moe_version(void);
  * act and y_perm then hold R + N rows and there is no separate y_shared. */
 size_t moe_workspace_size(const moe_config* cfg);
 
-/* Zero the start of the workspace, up to 1 KiB (the device error word, and the
- * counters of the 8-bit products).  Call once after allocating a workspace,
- * before its first use. */
+/* Zero the workspace header (the device error word and the products' tile
+ * counters).  Call once after allocating a workspace, before its first use; one
+ * workspace may serve the bf16 and the 8-bit calls by turns. */
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, void* stream);
 
 /* Steps a1-a3: RMSNorm, router and top-k selection.

@@ -87,7 +87,16 @@ constexpr int F_WIDE_ROWS = 256;
 constexpr int F_OUT_PITCH = 80;                       // bytes per row of a warp's output block of 64-byte rows
 constexpr int F_OUT_BYTES = 16 * F_OUT_PITCH;         // swapped: 16 rows of 32 bf16
 constexpr int F_OUT_WIDE_BYTES = 2048;                // wide: 16 rows of 128 bytes, or 32 of 64
-constexpr int F_CLAIM_WORD = 40, F_DONE_WORD = 41;    // header words: tiles claimed, pairs finished
+// Words of the workspace header (0-3: the error record, 32: the bf16 products' tile
+// counter): tiles claimed, pairs finished, and the finished parts of up to 50 cut
+// tiles, all of which every launch leaves at zero.  They are in the header, which no
+// other call of the library uses as scratch.
+constexpr int F_CLAIM_WORD = 40, F_DONE_WORD = 41;
+constexpr int F_SPLIT_TILES = 50;
+__host__ __device__ constexpr int f8_split_word(int tile) { return tile < 28 ? 4 + tile : 14 + tile; }
+static_assert(f8_split_word(27) < 32 && f8_split_word(28) > F_DONE_WORD &&
+                  f8_split_word(F_SPLIT_TILES - 1) < (int)kHeaderBytes / 4,
+              "counters inside the header, apart from its other words");
 
 // Rows of scale products per slot of 256 (swapped), and floats of a slot.
 template <int EPI, bool WIDE>
@@ -115,7 +124,6 @@ struct Fp8Args {
   int splits;              // parts that a tile's k-blocks are cut into
   unsigned split_magic;    // floor(2^32 / splits) + 1: its high product with an index is the index / splits
   int split_nk, split_rem; // k-blocks per part, one more in the first split_rem parts
-  unsigned* split_count;   // [tiles] parts done
   float4* partial;         // [tiles][splits][2][partial_vecs][256]
   int partial_vecs;        // float4 per thread and part
   int n_o;                 // weight tiles per group
@@ -993,7 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             unsigned count;
             asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
                          : "=r"(count)
-                         : "l"(args.split_count + tl.index), "r"((unsigned)args.splits - 1u)
+                         : "l"(args.hdr + f8_split_word(tl.index)), "r"((unsigned)args.splits - 1u)
                          : "memory");
             const bool last = count == (unsigned)args.splits - 1u;
             last_sh = last;
@@ -1455,7 +1463,8 @@ static Fp8Shape f8_shape(bool swiglu, int64_t rows, int groups, bool offsets, in
   int64_t best = f.wide ? 42 * nk : INT64_MAX;
   for (int chunk = moe::F_CHUNK; chunk >= 32 && tiles(chunk) <= pairs; chunk /= 2) {
     const int64_t r = std::min<int64_t>(chunk, per_group), t = tiles(chunk);
-    for (int64_t parts = 1; parts <= std::min(pairs / t, nk / 2) || parts == 1; ++parts) {
+    const int64_t most = t <= moe::F_SPLIT_TILES ? std::max<int64_t>(1, std::min(pairs / t, nk / 2)) : 1;
+    for (int64_t parts = 1; parts <= most; ++parts) {
       const int64_t cost = (26 + r * r / 2400) * ((nk + parts - 1) / parts) + (parts > 1 ? 300 + 6 * r + 25 * parts : 0);
       if (cost >= best) continue;
       best = cost;
@@ -1522,7 +1531,6 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   args.n_o = shape.n_o;
   args.chunk = shape.chunk;
   args.splits = 1;
-  args.split_count = nullptr;
   args.partial = nullptr;
   args.partial_vecs = f8_partial_vecs(shape, g.max_rows);
   const size_t split_bytes = gemm_fp8_split_bytes(swiglu, g.max_rows, groups, g.offsets != nullptr, g.nout, g.k);
@@ -1531,7 +1539,6 @@ moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
     args.split_magic = (unsigned)((1ull << 32) / (unsigned)args.splits + 1);  // exact: there are few tiles
     args.split_nk = args.nk / args.splits;
     args.split_rem = args.nk % args.splits;
-    args.split_count = reinterpret_cast<unsigned*>(g.hdr) + moe::kHeaderBytes / 4;
     args.partial = static_cast<float4*>(g.split_ws);
   }
   args.view = view ? 1 : 0;

@@ -31,13 +31,12 @@ struct Fp8Gemm {
   void* c = nullptr;         // [max_rows][nout]
   float* c_scale = nullptr;  // EPI_SWIGLU: [max_rows][ceil(nout / 128)]
   bool follows = false;      // the launch before it on the stream is the product that makes a: its end may overlap
-  int32_t* hdr = nullptr;    // workspace header and, behind it, the counters of cut tiles (kFp8HeaderBytes)
+  int32_t* hdr = nullptr;    // workspace header
   void* split_ws = nullptr;  // partial sums of cut tiles
   size_t split_bytes = 0;
 };
 
-// Start of every workspace of the 8-bit products: the header and the counters of
-// tiles cut along K, all zeroed by moe_workspace_init.
+// Start of every workspace of the 8-bit products, the header in it.
 constexpr size_t kFp8HeaderBytes = 1024;
 
 // Bytes of partial sums for these sizes (0: no tile is cut).  A launch with fewer

@@ -4,7 +4,6 @@
 // synchronises.
 
 #include "moe_common.cuh"
-#include "gemm_fp8_kernels.h"
 #include "moe_kernels.h"
 #include "tcgen05.cuh"
 
@@ -131,10 +130,6 @@ static moe_status check_common(const moe_config* c, const void* ws, size_t ws_by
     if (_st != MOE_OK) return _st; \
   } while (0)
 
-// The header and, in a workspace of the 8-bit products, the counters behind it
-// (in other workspaces those bytes are scratch that each call writes first).
-static size_t init_bytes(size_t ws_bytes) { return ws_bytes < kFp8HeaderBytes ? ws_bytes : kFp8HeaderBytes; }
-
 static inline char* wsp(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
 
 // a2 on the tensor cores pays off once there are many tokens and experts;
@@ -221,7 +216,7 @@ size_t moe_workspace_size(const moe_config* cfg) {
 
 moe_status moe_workspace_init(void* ws, size_t ws_bytes, void* stream) {
   if (ws == nullptr || ws_bytes < moe::kHeaderBytes || ((uintptr_t)ws % 256) != 0) return MOE_ERR_INVALID_ARG;
-  if (cudaMemsetAsync(ws, 0, init_bytes(ws_bytes), (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
+  if (cudaMemsetAsync(ws, 0, moe::kHeaderBytes, (cudaStream_t)stream) != cudaSuccess) return MOE_ERR_CUDA;
   return MOE_OK;
 }
 
@@ -400,7 +395,7 @@ moe_status moe_check_device_error(void* ws, size_t ws_bytes, void* stream, int32
     for (int i = 0; i < 4; ++i) info[i] = h[i];
   }
   if (h[0] != 0) {
-    if (cudaMemsetAsync(ws, 0, init_bytes(ws_bytes), s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, moe::kHeaderBytes, s) != cudaSuccess) return MOE_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
     return (moe_status)h[0];
   }

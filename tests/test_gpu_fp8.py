@@ -419,6 +419,25 @@ def test_expert_ffn(env, out, sizes, d, h):
     assert moe.moe_check_device_error(ws)[0] == 0
 
 
+def test_a_workspace_shared_with_other_calls(env):
+    """Products cut along K count their parts in the header: scratch that other calls leave behind it does not matter."""
+    torch, moe = env
+    n, k = 2048, 8192
+    aq, as_, bq, bs = _operands(torch, [9], n, k)
+    size = moe.library().moe_workspace_size_gemm_fp8(1, 9, n, k)
+    assert size > 4096
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    assert moe.library().moe_workspace_init(ws.data_ptr(), size, None) == 0
+    torch.cuda.synchronize()
+    own, c = torch.empty(9, n, device="cuda"), torch.empty(9, n, device="cuda")
+    moe.moe_gemm_fp8(1, None, 9, n, k, aq, as_, bq, bs, "f32", own, moe.workspace_gemm_fp8(1, 9, n, k))
+    for fill in (0xFF, 0x00, 0x5A):
+        ws[256:] = fill
+        moe.moe_gemm_fp8(1, None, 9, n, k, aq, as_, bq, bs, "f32", c, ws)
+        assert torch.equal(c, own)
+    assert moe.moe_check_device_error(ws)[0] == 0
+
+
 def test_ffn_in_a_workspace_of_more_tokens(env):
     """Fewer tokens may want more room for partial sums than more do: the call then does without."""
     torch, moe = env
