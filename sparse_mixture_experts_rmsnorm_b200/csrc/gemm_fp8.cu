@@ -1042,9 +1042,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         const int r_cta = quarter * 32;                          // this warp's rows of the CTA's 128
         const int valid = tl.rows - ((int)rank * 128 + r_cta);   // ... of which this many exist
         if (valid <= 0) {
+          // (so does the quarter's other warp: half_bar and half_sh's buffer stay as they are)
           ok = f8_pass_over(drain, tl.nk, args, &abort_flag);
           if (!ok) break;
-          if constexpr (SWIGLU) ++tiles_done;  // both warps of the quarter pass the tile over
           continue;
         }
         uint64_t acc[8][8];
@@ -1114,14 +1114,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
               m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
             }
           // the other half of the row's 128 units is with the warp of the same rows.
-          // Two buffers: that warp reads this tile's value before it arrives for the next.
-          float* at = &half_sh[tiles_done & 1u][0][r_cta + lane];
+          // Two buffers, one per phase of half_bar: that warp reads this tile's value before
+          // it arrives for the next one of the quarter's tiles that has rows.
+          float* at = &half_sh[half_phase][0][r_cta + lane];
           at[hf * 128] = m;
           __syncwarp();
           if (lane == 0) mbar_arrive(&half_bar[quarter]);
           if (!f8_warp_wait<false>(&half_bar[quarter], half_phase, args, &abort_flag, F_SITE_AMAX)) break;
           half_phase ^= 1u;
-          ++tiles_done;
           const float scale = quant_scale(fmaxf(m, at[(hf ^ 1) * 128]));
           const float inv = __frcp_rn(scale);
           if (hf == 0 && lane < valid) args.c_scale[(row + lane) * args.n_o + tl.o] = scale;
