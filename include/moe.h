@@ -367,8 +367,9 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
 size_t moe_workspace_size_fp8(const moe_config* cfg);
 
 /* moe_expert_ffn on e4m3 operands: per group g,
- *   t = silu(x . w_gate[g]) * (x . w_up[g]) in fp32, quantised per row and 128
- *   hidden units as moe_quantize_fp8 does, and y = t . w_down[g],
+ *   t = silu(x . w_gate[g]) * (x . w_up[g]) in fp32 (silu's exponential and
+ *   division each off by at most 2 ulp; 0 below -87.3), quantised per row and
+ *   128 hidden units as moe_quantize_fp8 does, and y = t . w_down[g],
  * every product as in moe_gemm_fp8.  Groups, offsets and rows as there;
  * x [max_rows][d] e4m3, its rows ldx >= d bytes apart (ldx % 16 == 0), with
  * x_scale [max_rows][ceil(d/128)], y [max_rows][d] in the act dtype.

@@ -1,0 +1,41 @@
+"""Values and inputs at which the e4m3 calls go wrong most easily."""
+import pytest
+
+import fp8_helpers as f8
+from test_gpu_fp8 import env  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [60, 2048])
+def test_activation_is_fp32_at_every_gate(env, rows):
+    """silu(gate) * up from -80 to 80, through the scale of a block whose only value it is (its code is 448).
+
+    In units of 2^-24 of the value: the exponential and the division are off by at most 2 ulp (4 units each), and
+    1 + e^-g, the product with up, amax / 448 and 448 * scale are rounded once each: 12.  Gate and up are exact.  60 rows
+    take the tiling with rows on the MMA's N side, 2048 the one with rows on its M side; the last row's gates of -500
+    and 500 give 0 and 250000."""
+    torch, moe = env
+    d, h = 128, 2048
+    v = torch.exp(torch.linspace(-7.0, 4.38, rows, device="cuda", dtype=torch.float64)).float()  # 0.0009 to 79.8
+    v[-1] = 500.0
+    x = torch.zeros(rows, d, device="cuda")
+    x[:, 0] = 1.0
+    gate, up = torch.zeros(2, 1, h, d, device="cuda")
+    gate[0, 0::256, 0], gate[0, 128::256, 0] = -1.0, 1.0  # the first hidden unit of each block of 128
+    up[0, ::128, 0] = 1.0
+    down = torch.zeros(1, d, h, device="cuda")
+    n = torch.arange(d, device="cuda")
+    down[0, n, n % 16 * 128] = 1.0
+    ones = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    cfg = moe.Config(rows, d, 1, 1, h, dtype="f32")
+    y = torch.empty(rows, d, device="cuda")
+    gate, up, down = (w.to(f8.E4M3) for w in (gate, up, down))
+    moe.moe_expert_ffn_fp8(cfg, 1, None, rows, x.to(f8.E4M3), v[:, None].contiguous(), gate, ones(1, 16, 1), up,
+                           ones(1, 16, 1), down, ones(1, 1, 16), h, y, moe.workspace_fp8(cfg))
+    u = v.double()[:, None]
+    g = torch.where(n % 2 == 0, -1.0, 1.0) * u
+    want = g / (1.0 + torch.exp(-g)) * u
+    err = (y.double() - want).abs() - want.abs() * 12 * 2.0 ** -24
+    assert torch.all(y[-1, ::2] == 0)
+    assert torch.all(err[:-1] <= 0) and torch.all(err[-1] <= 1e-30)
