@@ -307,8 +307,9 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
   const void* stream_h = residual ? out : h;
   if (N > 0) {
     // the router reads xn in the act dtype, the experts its e4m3 form; few
-    // experts or tokens: the router's dot products ride along with a second norm
-    const bool tc = cfg->dtype == MOE_BF16 && E >= 64 && N >= 512;
+    // experts or tokens, or router weights that TMA cannot read: the router's dot
+    // products ride along with a second norm
+    const bool tc = cfg->dtype == MOE_BF16 && E >= 64 && N >= 512 && !misaligned({w->w_router});
     MOE_TRY(launch_add_rmsnorm(cfg->dtype, h, residual, w->norm_w, residual ? out : nullptr, tc ? xn : nullptr, xq,
                                xs, N, d, cfg->rms_eps, s));
     if (tc)

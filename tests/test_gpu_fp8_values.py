@@ -39,3 +39,35 @@ def test_activation_is_fp32_at_every_gate(env, rows):
     err = (y.double() - want).abs() - want.abs() * 12 * 2.0 ** -24
     assert torch.all(y[-1, ::2] == 0)
     assert torch.all(err[:-1] <= 0) and torch.all(err[-1] <= 1e-30)
+
+
+@pytest.mark.parametrize("n_tokens", [64, 600])
+def test_layer_takes_router_weights_of_any_alignment(env, n_tokens):
+    """Router weights that start 2 bytes off a 16-byte boundary, with out in the place of h: the layer runs as for few
+    tokens instead of refusing after it has written h + residual to out."""
+    torch, moe = env
+    d, e, k, f = 256, 64, 4, 128
+    cfg = moe.Config(n_tokens, d, e, k, f)
+    w = {"norm_w": (1 + 0.1 * torch.randn(d, device="cuda")).bfloat16()}
+    for name, shape in (("w_gate", (e, f, d)), ("w_up", (e, f, d)), ("w_down", (e, d, f))):
+        w[name], w[name + "_scale"] = f8.quantize(torch.randn(*shape, device="cuda") * 0.08, 128)
+    router = torch.randn(e, d, device="cuda").bfloat16() * 0.1
+    off = torch.empty(e * d + 8, device="cuda", dtype=torch.bfloat16)[1:1 + e * d].view(e, d)
+    off.copy_(router)
+    assert router.data_ptr() % 16 == 0 and off.data_ptr() % 16 == 2
+    h, res = (torch.randn(n_tokens, d, device="cuda").bfloat16() for _ in range(2))
+    bias = torch.zeros(e, device="cuda")
+    got, idx = [], []
+    for r in (router, off):
+        out = h.clone()
+        idx.append(torch.empty(n_tokens, k, dtype=torch.int32, device="cuda"))
+        ws = moe.workspace_fp8(cfg)
+        moe.moe_layer_forward_fp8(cfg, {**w, "w_router": r}, out, res, bias, out, ws, routing=dict(topk_idx=idx[-1]))
+        assert moe.moe_check_device_error(ws)[0] == 0
+        got.append(out.double())
+    # the two routers sum in different orders: a token whose scores nearly tie may choose otherwise
+    same = (idx[0] == idx[1]).all(1)
+    assert float(same.double().mean()) >= 0.99
+    # and its gates differ by 2^-24 d of the logits' absolute sums at most, which moves a bf16 result by a step at most
+    diff = (got[0] - got[1])[same].abs()
+    assert torch.all(diff <= got[0][same].abs() * 2.0 ** -7 + 1e-4)
