@@ -265,11 +265,14 @@ def _weights_struct(w: dict) -> MoeWeights:
                         ("norm_w", "w_router", "w_gate", "w_up", "w_down", "ws_gate", "ws_up", "ws_down")])
 
 
+def _routing_tensors(routing: dict | None):
+    return [(routing or {}).get(n) for n, _ in MoeRouting._fields_]
+
+
 def _routing_struct(routing: dict | None):
     if routing is None:
         return None
-    return MoeRouting(*[_ptr(routing.get(n)) for n in
-                        ("scores", "topk_idx", "topk_gate", "counts", "offsets", "slot_row", "row_token")])
+    return MoeRouting(*[_ptr(t) for t in _routing_tensors(routing)])
 
 
 def _trace_struct(trace: dict | None, stream):
@@ -376,7 +379,8 @@ def moe_layer_forward_fp8(cfg: Config, weights: dict, h, residual, bias, out, ws
                                       _ptr(out), ctypes.byref(r) if r is not None else None,
                                       ctypes.byref(tr) if tr is not None else None,
                                       _ptr(ws), ws.numel(),
-                                      _stream_of(stream, *mats, h, residual, bias, out, ws)),
+                                      _stream_of(stream, *mats, h, residual, bias, out, ws,
+                                                 *_routing_tensors(routing))),
            "moe_layer_forward_fp8")
 
 

@@ -71,3 +71,23 @@ def test_layer_takes_router_weights_of_any_alignment(env, n_tokens):
     # and its gates differ by 2^-24 d of the logits' absolute sums at most, which moves a bf16 result by a step at most
     diff = (got[0] - got[1])[same].abs()
     assert torch.all(diff <= got[0][same].abs() * 2.0 ** -7 + 1e-4)
+
+
+@pytest.mark.parametrize("name", ["scores", "topk_idx", "topk_gate", "counts", "offsets", "slot_row", "row_token"])
+def test_layer_refuses_routing_outputs_off_the_device(env, name):
+    """On the host, before anything is launched: out stays as it was."""
+    torch, moe = env
+    cfg = moe.Config(4, 128, 2, 1, 16)
+    shapes = dict(scores=(4, 2), topk_idx=(4, 1), topk_gate=(4, 1), counts=(2,), offsets=(3,), slot_row=(4,), row_token=(4,))
+    kind = torch.float32 if name in ("scores", "topk_gate") else torch.int32
+    codes = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    ones = lambda *s: torch.ones(*s, device="cuda")  # noqa: E731
+    w = dict(norm_w=ones(128).bfloat16(), w_router=ones(2, 128).bfloat16(), w_gate=codes(2, 16, 128),
+             w_gate_scale=ones(2, 1, 1), w_up=codes(2, 16, 128), w_up_scale=ones(2, 1, 1), w_down=codes(2, 128, 16),
+             w_down_scale=ones(2, 1, 1))
+    out = ones(4, 128).bfloat16() * 7
+    with pytest.raises(ValueError):
+        moe.moe_layer_forward_fp8(cfg, w, ones(4, 128).bfloat16(), None, None, out, moe.workspace_fp8(cfg),
+                                  routing={name: torch.zeros(shapes[name], dtype=kind)})
+    torch.cuda.synchronize()
+    assert torch.all(out == 7)
