@@ -336,20 +336,25 @@ def moe_quantize_fp8(dtype: str, block_rows: int, n_mats: int, rows: int, cols: 
 
 
 def _rows(t, cols: int):
-    """(pointer, bytes between rows) of a matrix of one-byte elements whose rows may lie apart."""
+    """(pointer, bytes between rows) of a matrix of one-byte elements, of whose rows the first cols columns are read;
+    they may lie apart.  (Other than two dimensions, or a raw pointer: packed rows of cols.)"""
     if t is None or isinstance(t, int):
         return t, cols
-    if t.dim() != 2 or t.is_contiguous():
+    if t.dim() != 2:
         return _ptr(t), cols
+    if t.element_size() != 1:
+        raise ValueError("a matrix of codes passed to the MoE library must have one-byte elements")
+    if t.shape[1] < cols:
+        raise ValueError(f"a matrix passed to the MoE library has {t.shape[1]} columns of the {cols} that are read")
     if t.stride(1) != 1 and t.shape[1] > 1:
         raise ValueError("the rows of a matrix passed to the MoE library must be contiguous")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols
 
 
 def moe_gemm_fp8(n_groups: int, offsets, max_rows: int, n_out: int, k: int, a, a_scale, b, b_scale, c_dtype: str, c,
                  ws, stream=None):
     """Rows [offsets[g], offsets[g+1]) of a times b[g]^T, e4m3 with block scales; offsets None: one group.
-    The rows of a may lie apart (a slice of a wider buffer)."""
+    The rows of a may lie apart (a wider buffer, or a slice of one)."""
     a_ptr, lda = _rows(a, k)
     _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, a_ptr, lda, _ptr(a_scale), _ptr(b),
                              _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(),

@@ -91,3 +91,28 @@ def test_layer_refuses_routing_outputs_off_the_device(env, name):
                                   routing={name: torch.zeros(shapes[name], dtype=kind)})
     torch.cuda.synchronize()
     assert torch.all(out == 7)
+
+
+def test_rows_of_a_wider_buffer_given_whole(env):
+    """A contiguous matrix wider than k (or d_model) is read at its own pitch, like the slice of it."""
+    torch, moe = env
+    rows, n, k = 200, 256, 400
+    a, sa = f8.quantize(torch.randn(rows, k, device="cuda"), 1)
+    b, sb = f8.quantize(torch.randn(2, 1, n, k, device="cuda") * 0.05, 128)
+    down, sd = f8.quantize(torch.randn(1, k, n, device="cuda") * 0.05, 128)
+    wide = torch.full((rows, 512), 0x7F, dtype=torch.uint8, device="cuda").view(f8.E4M3)  # NaN behind the columns
+    wide[:, :k] = a
+    ws = moe.workspace_gemm_fp8(1, rows, n, k)
+    c = torch.empty(3, rows, n, device="cuda")
+    for x, out in ((a, c[0]), (wide, c[1]), (wide[:, :k], c[2])):
+        moe.moe_gemm_fp8(1, None, rows, n, k, x, sa, b[0], sb[0], "f32", out, ws)
+    assert torch.isfinite(c).all() and torch.equal(c[0], c[1]) and torch.equal(c[0], c[2])
+    one = torch.empty(1, n, device="cuda")
+    moe.moe_gemm_fp8(1, None, 1, n, k, wide[5:6], sa[5:6], b[0], sb[0], "f32", one, ws)  # one row has no pitch
+    assert torch.isfinite(one).all()
+    cfg = moe.Config(rows, k, 1, 1, n)
+    ws = moe.workspace_fp8(cfg)
+    y = torch.empty(3, rows, k, dtype=torch.bfloat16, device="cuda")
+    for x, out in ((a, y[0]), (wide, y[1]), (wide[:, :k], y[2])):
+        moe.moe_expert_ffn_fp8(cfg, 1, None, rows, x, sa, b[0], sb[0], b[1], sb[1], down, sd, n, out, ws)
+    assert torch.isfinite(y).all() and torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
