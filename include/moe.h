@@ -327,7 +327,8 @@ typedef struct {
  *   residual), xn [N][d] (may equal x or residual, not res_out), q [N][d] with
  *   q_scale [N][ceil(d/128)] (both or neither).
  * Any d up to 49152, odd ones included; cfg gives N, d, dtype and rms_eps.
- * MOE_ERR_INVALID_ARG when no output is wanted or only one of q, q_scale. */
+ * MOE_ERR_INVALID_ARG when no output is wanted, only one of q, q_scale, or xn
+ * is res_out. */
 moe_status moe_add_rmsnorm(const moe_config* cfg, const void* x, const void* residual, const void* norm_w,
                            void* res_out, void* xn, void* q, float* q_scale, void* stream);
 

@@ -173,6 +173,7 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, const void* x, const void* res
   if (cfg->d_model > 49152) return MOE_ERR_UNSUPPORTED;
   if (cfg->n_tokens == 0) return MOE_OK;  // empty tensors may have NULL pointers
   if (!x || !norm_w || (!res_out && !xn && !q) || (q == nullptr) != (q_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (xn && xn == res_out) return MOE_ERR_INVALID_ARG;
   return launch_add_rmsnorm(cfg->dtype, x, residual, norm_w, res_out, xn, (uint8_t*)q, q_scale, cfg->n_tokens,
                             cfg->d_model, cfg->rms_eps, (cudaStream_t)stream);
 }

@@ -22,3 +22,16 @@ def test_row_operands_that_are_too_narrow_or_not_of_codes():
     for wrong in (codes.bfloat16(), codes.bfloat16()[:, :32]):
         with pytest.raises(ValueError, match="one-byte"):
             gemm(wrong, 32)
+
+
+def test_norm_refuses_one_place_for_both_outputs():
+    """xn and res_out hold different values: the same place is refused; either may be an input's place."""
+    lib = moe.library()
+    cfg = moe.Config(64, 256, 8, 2, 128).c()
+
+    def norm(x, res, res_out, xn):
+        return lib.moe_add_rmsnorm(cfg, x, res, 1 << 16, res_out, xn, None, None, None)
+
+    assert norm(4096, 8192, 256, 256) == moe.MOE_ERR_INVALID_ARG
+    assert norm(4096, 8192, 4096, 4096) == moe.MOE_ERR_INVALID_ARG
+    assert norm(4096, None, 4096, 4096) == moe.MOE_ERR_INVALID_ARG
