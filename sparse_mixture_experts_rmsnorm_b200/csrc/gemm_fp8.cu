@@ -994,8 +994,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
         if (leader) {
           if (!f8_warp_wait<true>(&pair_bar, ph, args, &abort_flag, F_SITE_SPLIT)) return 0;
           if (lane == 0) {
-            // after the barriers: releases, and acquires, for every thread of the pair's
-            // epilogues; the count goes back to zero for the next launch
+            // after the barriers: releases the sums of every thread of the pair's epilogues,
+            // and acquires those of the other parts, which the releasing arrivals on both
+            // CTAs' done_bar pass on to them; the count goes back to zero for the next launch
             unsigned count;
             asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
                          : "=r"(count)
@@ -1005,7 +1006,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             last_sh = last;
             mbar_arrive(&done_bar);
             const uint32_t peer_done = map_to_rank(&done_bar, 1);
-            mbar_arrive_expect_tx_cluster(peer_done, 4);
+            mbar_arrive_expect_tx_cluster_release(peer_done, 4);
             st_async_b32(map_to_rank((const void*)&last_sh, 1), last, peer_done);
           }
         } else if (lane == 0) {

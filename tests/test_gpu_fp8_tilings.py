@@ -69,3 +69,20 @@ def test_wide_ffn_of_one_block_along_k_with_tiles_whose_last_rows_are_missing(en
     the rows' largest magnitudes pass between the warps with nothing but their own barrier to order them."""
     torch, moe = env
     _check_codes(torch, moe, [270, 256, 300, 0, 520, 257, 512, 269], 128, 2048, repeats=8)
+
+
+@pytest.mark.parametrize("rows,n,k", [(1, 512, 8192), (24, 1024, 7168), (5, 2000, 16384)])
+def test_parts_of_every_column_meet_in_order(env, rows, n, k):
+    """Tiles cut along K, both CTAs of a pair holding columns of each: the operands are small whole numbers whose sums are
+    exact, so every result has the sum of all parts and nothing else, call after call on changing operands."""
+    torch, moe = env
+    assert moe.library().moe_workspace_size_gemm_fp8(1, rows, n, k) > 4096  # parts are held
+    ws = moe.workspace_gemm_fp8(1, rows, n, k)
+    sa, sb = torch.ones(rows, f8.blocks(k), device="cuda"), torch.ones(1, f8.blocks(n), f8.blocks(k), device="cuda")
+    c = torch.empty(rows, n, device="cuda")
+    for i in range(50):
+        a = torch.randint(-2, 3, (rows, k), device="cuda").float()
+        b = torch.randint(-2, 3, (1, n, k), device="cuda").float()
+        moe.moe_gemm_fp8(1, None, rows, n, k, a.to(f8.E4M3), sa, b.to(f8.E4M3), sb, "f32", c, ws)
+        assert torch.equal(c.double(), a.double() @ b[0].double().T), i  # |sums| <= 4 k < 2^24
+    assert moe.moe_check_device_error(ws)[0] == 0
