@@ -257,6 +257,14 @@ __device__ __forceinline__ bool f8_warp_wait(uint64_t* bar, uint32_t parity, con
   return __all_sync(0xffffffffu, ok);
 }
 
+// mbar_arrive_expect_tx_cluster with a release: what this thread has done and observed
+// so far (an acquired count, with all that it stands for) is passed on to the waiters.
+__device__ __forceinline__ void f8_arrive_expect_tx_release(uint32_t bar_cluster, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
+               "r"(bytes)
+               : "memory");
+}
+
 // ---- TMA, MMA and TMEM ----------------------------------------------------------
 __device__ __forceinline__ void f8_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   tma_load_2d_pair(dst, map, bar, c0, c1);
@@ -1006,7 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(F_THREADS, 1)
             last_sh = last;
             mbar_arrive(&done_bar);
             const uint32_t peer_done = map_to_rank(&done_bar, 1);
-            mbar_arrive_expect_tx_cluster_release(peer_done, 4);
+            f8_arrive_expect_tx_release(peer_done, 4);
             st_async_b32(map_to_rank((const void*)&last_sh, 1), last, peer_done);
           }
         } else if (lane == 0) {

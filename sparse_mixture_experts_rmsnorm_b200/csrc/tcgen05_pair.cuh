@@ -102,13 +102,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar_clust
                "r"(bytes)
                : "memory");
 }
-// The same with a release: what this thread has done and observed so far (an
-// acquired count, with all that it stands for) is passed on to the waiters.
-__device__ __forceinline__ void mbar_arrive_expect_tx_cluster_release(uint32_t bar_cluster, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar_cluster),
-               "r"(bytes)
-               : "memory");
-}
 // Store one word into the other CTA's shared memory; its barrier counts the 4
 // bytes as transferred once the word is written, so a reader that sees the
 // barrier's phase complete (acquire at cluster scope) sees the word.
