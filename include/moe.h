@@ -297,7 +297,8 @@ moe_status moe_compute_load_stats(const moe_config* cfg, const int32_t* counts, 
  * weights [G][N][K] are [G][ceil(N / 128)][ceil(K / 128)].  Any positive scales
  * are taken as they are: they need not come from moe_quantize_fp8.
  * Products: K % 16 == 0 and 16-byte aligned code pointers (TMA), else
- * MOE_ERR_UNSUPPORTED.
+ * MOE_ERR_UNSUPPORTED; so are more than 0x7fffff00 rows, columns or weight rows
+ * of all groups together, and rows 2^40 bytes apart.
  * ------------------------------------------------------------------------- */
 
 /* The layer's weights with e4m3 expert matrices (same shapes as moe_weights). */
@@ -334,7 +335,8 @@ moe_status moe_add_rmsnorm(const moe_config* cfg, const void* x, const void* res
 
 /* n_mats matrices [rows][cols] (bf16 or fp32, dtype a moe_dtype) to e4m3 in
  * blocks of block_rows x 128, block_rows = 1 (activations) or 128 (weights).
- *   q [n_mats][rows][cols],  scale [n_mats][ceil(rows/block_rows)][ceil(cols/128)]. */
+ *   q [n_mats][rows][cols],  scale [n_mats][ceil(rows/block_rows)][ceil(cols/128)].
+ * More than 0x7fffff00 columns are MOE_ERR_UNSUPPORTED. */
 moe_status moe_quantize_fp8(int32_t dtype, int32_t block_rows, int32_t n_mats, int32_t rows, int32_t cols,
                             const void* x, void* q, float* scale, void* stream);
 

@@ -184,6 +184,7 @@ moe_status moe_quantize_fp8(int32_t dtype, int32_t block_rows, int32_t n_mats, i
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
   if ((block_rows != 1 && block_rows != 128) || n_mats < 0 || rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (n_mats > 0 && rows > 0 && (!x || !q || !scale)) return MOE_ERR_INVALID_ARG;
+  if (cols > kFp8MostExtent) return MOE_ERR_UNSUPPORTED;
   return launch_quantize(dtype, block_rows, n_mats, rows, cols, x, (uint8_t*)q, scale, (cudaStream_t)stream);
 }
 
@@ -203,7 +204,9 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
   if (ws == nullptr || ((uintptr_t)ws % 256) != 0) return MOE_ERR_INVALID_ARG;
   if (max_rows > 0 && (!a || !a_scale || !b || !b_scale || !c)) return MOE_ERR_INVALID_ARG;
   if (lda < k) return MOE_ERR_INVALID_ARG;
-  if (k % 16 || lda % 16 || misaligned({a, b}) || (int64_t)n_groups * n_out > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (k % 16 || lda % 16 || lda >= kFp8MostStride || misaligned({a, b})) return MOE_ERR_UNSUPPORTED;
+  if (max_rows > kFp8MostExtent || k > kFp8MostExtent || (int64_t)n_groups * n_out > kFp8MostExtent)
+    return MOE_ERR_UNSUPPORTED;
   if (ws_bytes < kFp8HeaderBytes) return MOE_ERR_WORKSPACE;  // (with no room for parts, no tile is cut)
   Fp8Gemm g;
   g.epi = c_dtype == MOE_BF16 ? EPI_STORE : EPI_F32;
@@ -235,7 +238,7 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
   MOE_TRY(check_fp8(cfg, ws, ws_bytes));
   if (n_groups < 1 || n_groups > moe::TC_MAX_GROUPS || max_rows < 0 || d_ff < 1) return MOE_ERR_INVALID_ARG;
   if (offsets == nullptr && n_groups != 1) return MOE_ERR_INVALID_ARG;
-  if (d_ff % 16 || (int64_t)n_groups * d_ff > 0x7fffffffLL || (int64_t)n_groups * cfg->d_model > 0x7fffffffLL)
+  if (d_ff % 16 || max_rows > kFp8MostExtent || (int64_t)n_groups * std::max(d_ff, cfg->d_model) > kFp8MostExtent)
     return MOE_ERR_UNSUPPORTED;
   const Fp8Layout L = fp8_layout_in(cfg, ws_bytes);
   if ((int64_t)max_rows * d_ff > L.act_elems || (int64_t)max_rows * q_blocks(d_ff) > L.act_scales)
@@ -244,7 +247,8 @@ moe_status moe_expert_ffn_fp8(const moe_config* cfg, int32_t n_groups, const int
   if (!x || !x_scale || !w_gate || !w_gate_scale || !w_up || !w_up_scale || !w_down || !w_down_scale || !y)
     return MOE_ERR_INVALID_ARG;
   if (ldx < cfg->d_model) return MOE_ERR_INVALID_ARG;
-  if (ldx % 16 || misaligned({x, w_gate, w_up, w_down}) || !one_view(w_gate, w_up)) return MOE_ERR_UNSUPPORTED;
+  if (ldx % 16 || ldx >= kFp8MostStride || misaligned({x, w_gate, w_up, w_down}) || !one_view(w_gate, w_up))
+    return MOE_ERR_UNSUPPORTED;
   Fp8Gemm p;
   p.a = operand(x, x_scale, ldx);
   p.b = operand(w_gate, w_gate_scale);
@@ -273,11 +277,11 @@ moe_status moe_layer_forward_fp8(const moe_config* cfg, const moe_weights_fp8* w
     if (misaligned({w->w_gate, w->w_up, w->w_down}) || (shared && misaligned({w->ws_gate, w->ws_up, w->ws_down})))
       return MOE_ERR_UNSUPPORTED;
     if (!one_view(w->w_gate, w->w_up) || (shared && !one_view(w->ws_gate, w->ws_up))) return MOE_ERR_UNSUPPORTED;
-    if ((int64_t)E * H > 0x7fffffffLL || (int64_t)E * d > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+    if ((int64_t)E * std::max(H, d) > kFp8MostExtent || cfg->d_ff_shared > kFp8MostExtent) return MOE_ERR_UNSUPPORTED;
   }
   cudaStream_t s = (cudaStream_t)stream;
   const Fp8Layout L = fp8_layout_in(cfg, ws_bytes);
-  if (L.rows + N > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
+  if (L.rows + N > kFp8MostExtent) return MOE_ERR_UNSUPPORTED;
   auto pick = [&](void* user, size_t off) { return user ? user : (void*)wsp(ws, off); };
   void* xn = wsp(ws, L.xn);
   uint8_t* xq = (uint8_t*)wsp(ws, L.xq);

@@ -1460,7 +1460,7 @@ static Fp8Shape f8_shape(bool swiglu, int64_t rows, int groups, bool offsets, in
   Fp8Shape f;
   f.wide = rows >= (int64_t)moe::F_WIDE_ROWS * groups;
   f.chunk = moe::F_CHUNK;
-  f.n_o = swiglu ? (nout + 127) / 128 : (nout + 255) / 256;
+  f.n_o = (int)(swiglu ? ((int64_t)nout + 127) / 128 : ((int64_t)nout + 255) / 256);
   f.splits = 1;
   auto tiles = [&](int chunk) { return ((rows + chunk - 1) / chunk + (offsets ? groups : 0)) * f.n_o; };
   f.tiles = tiles(f.chunk);

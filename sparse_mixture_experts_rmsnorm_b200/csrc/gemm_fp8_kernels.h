@@ -36,6 +36,12 @@ struct Fp8Gemm {
   size_t split_bytes = 0;
 };
 
+// Most rows, columns (of any operand) and weight rows of all groups: rounded up to
+// whole tiles, and a tile further, they still fit an int.
+constexpr int64_t kFp8MostExtent = 0x7fffff00;
+// Bytes between rows stay below a tensor map's largest stride.
+constexpr int64_t kFp8MostStride = (int64_t)1 << 40;
+
 // Start of every workspace of the 8-bit products, the header in it.
 constexpr size_t kFp8HeaderBytes = 1024;
 

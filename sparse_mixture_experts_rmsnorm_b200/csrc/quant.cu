@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kTileThreads<V>, kTileBlocks<V>)
   constexpr int STEP = kTileThreads<V> / ACROSS;  // rows per pass
   constexpr int PASSES = Q_BLOCK / STEP;          // 8 (V = 8, 4) or 32 (V = 1)
   __shared__ float part[2][16];
-  const int rb = (rows + Q_BLOCK - 1) / Q_BLOCK, cb = gridDim.x;
+  const int rb = rows / Q_BLOCK + (rows % Q_BLOCK != 0), cb = gridDim.x;
   const int tr = threadIdx.x / ACROSS;
   const int c = blockIdx.x * Q_BLOCK + (threadIdx.x % ACROSS) * V;
   int parity = 0;

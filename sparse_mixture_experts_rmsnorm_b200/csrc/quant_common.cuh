@@ -35,5 +35,5 @@ __device__ __forceinline__ uint8_t e4m3x1(float v) {
 }  // namespace moe
 
 namespace moe_host {
-inline int q_blocks(int cols) { return (cols + moe::Q_BLOCK - 1) / moe::Q_BLOCK; }
+inline int q_blocks(int cols) { return cols / moe::Q_BLOCK + (cols % moe::Q_BLOCK != 0); }
 }  // namespace moe_host
