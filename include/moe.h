@@ -364,6 +364,16 @@ moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_ro
                         const void* a, int64_t lda, const float* a_scale, const void* b, const float* b_scale,
                         int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream);
 
+/* The tiling that a product of these sizes takes on the current device (nothing
+ * is launched): tiling (host) receives
+ *   [0] 1: tiles of 256 rows of a group on the MMA's M side, 0: on its N side,
+ *   [1] most rows of a group in one tile,
+ *   [2] parts that a tile is cut into along K, given room for their sums.
+ * swiglu != 0: the gate and up product of moe_expert_ffn_fp8 (n_out = d_ff,
+ * k = d_model).  For tests and for reading measurements. */
+moe_status moe_gemm_fp8_tiling(int32_t swiglu, int32_t n_groups, int32_t has_offsets, int32_t max_rows, int32_t n_out,
+                               int32_t k, int32_t* tiling);
+
 /* Bytes of workspace for moe_expert_ffn_fp8 and moe_layer_forward_fp8 with
  * this config; 0 if it is invalid.  One sized for more tokens serves fewer
  * (room for partial sums as in moe_gemm_fp8). */

@@ -32,8 +32,8 @@ ENTRY_POINTS = (
     "moe_status_string", "moe_version", "moe_workspace_size", "moe_workspace_init", "moe_route", "moe_route_hash",
     "moe_permute", "moe_permute_noalloc", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_bias_update",
     "moe_compute_load_stats", "moe_add_rmsnorm", "moe_quantize_fp8", "moe_workspace_size_gemm_fp8", "moe_gemm_fp8",
-    "moe_workspace_size_fp8", "moe_expert_ffn_fp8", "moe_layer_forward_fp8", "moe_check_device_error", "moe_set_wait_timeout_ns", "moe_set_gemm_tiling",
-    "moe_selftest_wait_timeout",
+    "moe_gemm_fp8_tiling", "moe_workspace_size_fp8", "moe_expert_ffn_fp8", "moe_layer_forward_fp8",
+    "moe_check_device_error", "moe_set_wait_timeout_ns", "moe_set_gemm_tiling", "moe_selftest_wait_timeout",
 )
 
 
@@ -98,6 +98,7 @@ def _load():
         "moe_quantize_fp8": (I32, [I32, I32, I32, I32, I32, P, P, P, P]),
         "moe_workspace_size_gemm_fp8": (SZ, [I32, I32, I32, I32]),
         "moe_gemm_fp8": (I32, [I32, P, I32, I32, I32, P, I64, P, P, P, I32, P, P, SZ, P]),
+        "moe_gemm_fp8_tiling": (I32, [I32, I32, I32, I32, I32, I32, P]),
         "moe_workspace_size_fp8": (SZ, [cfgp]),
         "moe_expert_ffn_fp8": (I32, [cfgp, I32, P, I32, P, I64, P, P, P, P, P, P, P, I32, P, P, SZ, P]),
         "moe_layer_forward_fp8": (I32, [cfgp, ctypes.POINTER(MoeWeightsFp8), P, P, P, P, ctypes.POINTER(MoeRouting),
@@ -359,6 +360,14 @@ def moe_gemm_fp8(n_groups: int, offsets, max_rows: int, n_out: int, k: int, a, a
     _check(_lib.moe_gemm_fp8(n_groups, _ptr(offsets), max_rows, n_out, k, a_ptr, lda, _ptr(a_scale), _ptr(b),
                              _ptr(b_scale), _DTYPES[c_dtype], _ptr(c), _ptr(ws), ws.numel(),
                              _stream_of(stream, offsets, a, a_scale, b, b_scale, c, ws)), "moe_gemm_fp8")
+
+
+def moe_gemm_fp8_tiling(swiglu: bool, n_groups: int, has_offsets: bool, max_rows: int, n_out: int, k: int):
+    """(wide, most rows of a tile, parts along K) of a product of these sizes; nothing is launched."""
+    tiling = (ctypes.c_int32 * 3)()
+    _check(_lib.moe_gemm_fp8_tiling(int(swiglu), n_groups, int(has_offsets), max_rows, n_out, k, tiling),
+           "moe_gemm_fp8_tiling")
+    return bool(tiling[0]), tiling[1], tiling[2]
 
 
 def moe_expert_ffn_fp8(cfg: Config, n_groups: int, offsets, max_rows: int, x, x_scale, w_gate, w_gate_scale, w_up,

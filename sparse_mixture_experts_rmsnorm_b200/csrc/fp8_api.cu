@@ -194,6 +194,14 @@ size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n
                                     gemm_fp8_split_bytes(false, max_rows, n_groups, false, n_out, k));
 }
 
+moe_status moe_gemm_fp8_tiling(int32_t swiglu, int32_t n_groups, int32_t has_offsets, int32_t max_rows, int32_t n_out,
+                               int32_t k, int32_t* tiling) {
+  if (n_groups < 1 || n_groups > moe::TC_MAX_GROUPS || max_rows < 1 || n_out < 1 || k < 1) return MOE_ERR_INVALID_ARG;
+  if ((!has_offsets && n_groups != 1) || !tiling) return MOE_ERR_INVALID_ARG;
+  gemm_fp8_tiling(swiglu != 0, max_rows, n_groups, has_offsets != 0, n_out, k, tiling);
+  return MOE_OK;
+}
+
 moe_status moe_gemm_fp8(int32_t n_groups, const int32_t* offsets, int32_t max_rows, int32_t n_out, int32_t k,
                         const void* a, int64_t lda, const float* a_scale, const void* b, const float* b_scale,
                         int32_t c_dtype, void* c, void* ws, size_t ws_bytes, void* stream) {

@@ -1495,6 +1495,13 @@ size_t gemm_fp8_split_bytes(bool swiglu, int64_t rows, int groups, bool offsets,
   return f.splits == 1 ? 0 : (size_t)f.tiles * f.splits * 2 * f8_partial_vecs(f, rows) * 256 * sizeof(float4);
 }
 
+void gemm_fp8_tiling(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k, int32_t tiling[3]) {
+  const Fp8Shape f = f8_shape(swiglu, rows, groups, offsets, nout, k);
+  tiling[0] = f.wide;
+  tiling[1] = f.chunk;
+  tiling[2] = f.splits;
+}
+
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s) {
   if (g.max_rows == 0) return MOE_OK;
   const bool swiglu = g.epi == EPI_SWIGLU;

@@ -49,6 +49,10 @@ constexpr size_t kFp8HeaderBytes = 1024;
 // bytes does not cut its tiles.
 size_t gemm_fp8_split_bytes(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k);
 
+// The tiling of a launch whose partial sums have room: most rows of a tile, 256 of
+// them on the MMA's M side (wide) or fewer on its N side, and parts along K.
+void gemm_fp8_tiling(bool swiglu, int64_t rows, int groups, bool offsets, int nout, int k, int32_t tiling[3]);
+
 moe_status launch_gemm_fp8(const Fp8Gemm& g, cudaStream_t s);
 
 }  // namespace moe_host

@@ -67,3 +67,19 @@ def test_extents_that_tiles_would_carry_past_an_int_are_refused():
 def test_workspace_sizes_of_the_largest_extents(n, k):
     assert moe.library().moe_workspace_size_gemm_fp8(1, 1, n, k) % 256 == 0
     assert 1024 <= moe.library().moe_workspace_size_gemm_fp8(1, 1, n, k) < 1 << 40
+
+
+def test_tiling_of_a_product():
+    """The documented rule: groups averaging 256 rows are wide; few tiles get smaller or are cut."""
+    tiling = moe.moe_gemm_fp8_tiling
+    assert tiling(False, 1, False, 8192, 4096, 7168) == (True, 256, 1)
+    assert tiling(True, 256, True, 65536, 2048, 7168) == (True, 256, 1)
+    assert tiling(True, 256, True, 65535, 2048, 7168) == (False, 256, 1)
+    wide, rows, parts = tiling(False, 1, False, 1, 4096, 7168)
+    assert not wide and parts > 1
+    assert tiling(False, 1, False, 200, 2048, 7168) == (False, 32, 1)
+    for bad in ((False, 0, True, 1, 16, 16), (False, 2, False, 1, 16, 16), (False, 1, False, 0, 16, 16),
+                (False, 1, False, 1, 0, 16), (False, 1, False, 1, 16, 0), (True, 1025, True, 1, 16, 16)):
+        with pytest.raises(moe.MoEError):
+            tiling(*bad)
+    assert moe.library().moe_gemm_fp8_tiling(0, 1, 0, 1, 16, 16, None) == moe.MOE_ERR_INVALID_ARG
