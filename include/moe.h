@@ -354,7 +354,8 @@ size_t moe_workspace_size_gemm_fp8(int32_t n_groups, int32_t max_rows, int32_t n
  * once, to c_dtype (moe_dtype).
  *   n_groups G in [1, 1024];  offsets [G+1] device, nondecreasing,
  *   offsets[0] >= 0, offsets[G] <= max_rows; NULL = one group of max_rows rows
- *   (a plain product).  Groups may be empty.
+ *   (a plain product).  Groups may be empty.  The tiling is chosen from max_rows,
+ *   n_groups, n_out and k: a max_rows far above offsets[G] costs speed.
  *   a [max_rows][k], its rows lda >= k bytes apart (lda % 16 == 0),
  *   a_scale [max_rows][ceil(k/128)], b [G][n_out][k],
  *   b_scale [G][ceil(n_out/128)][ceil(k/128)], c [max_rows][n_out] out; rows

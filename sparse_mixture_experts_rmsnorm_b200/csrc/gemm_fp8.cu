@@ -23,9 +23,11 @@
 //           by column; in the 16x256b shape (lane l holds rows l / 4 and l / 4 + 8,
 //           columns 2 (l % 4) and + 1 of every eight) one product read from shared
 //           memory serves four values.
-// Measured on B200 with the MMAs running beside it, a 256 x 256 k-block of a pair
-// takes the epilogue about 460 cycles in the 32x32b shape and 980 in the 16x256b
-// shape (which moves half as much per access); the MMAs themselves take 512.
+// Measured on B200, the reads and additions of a 256 x 256 k-block of a pair take the
+// epilogue about 460 cycles in the 32x32b shape and 980 in the 16x256b shape (which
+// moves half as much per access), and its MMAs 512.  A whole wide k-block takes 0.42 us
+// (735 cycles) with one tile per pair and about 900 cycles in large calls, not the 512
+// that two slots would allow; which hand-over costs the rest has not been measured.
 //
 // Gate and up.  One view over both matrices (their distance is a stride)
 // interleaves them in shared memory, eight gate rows, eight up rows, so a thread
@@ -78,8 +80,10 @@ constexpr int F_SLOTS = 2;                            // rows of scale products,
 // readers of a published tile index: even CTA: MMA, 2 scale and 8 epilogue
 // warps; odd CTA: producer, 2 and 8
 constexpr int F_TRING_READERS = 22;
-// Rows a group from which on the wide tiling is taken.  It reads its accumulators
-// faster but works on 256 rows whatever a group has.  Expert FFN of 7168 x 2048 (or
+// Rows a group, on average over max_rows (the host knows no more), from which on the
+// wide tiling is taken.  It reads its accumulators faster but works on 256 rows whatever
+// a group has: of groups of 256 rows on average, half have a second tile of a few rows.
+// With nearly even groups, expert FFN of 7168 x 2048 (or
 // 4096 x 14336) in a steady loop, wide against swapped: 128 rows a group 507 and
 // 461 us, 141 rows 1002 and 948, 256 rows 5464 and 5482 (both at the power limit),
 // 1024 rows 1939 and 2290.
@@ -365,7 +369,7 @@ __device__ __forceinline__ int f8_scale_at(int c) {
 
 // silu(g) * u in fp32, silu(g) = g / (1 + e^-g): the full exponential and a division
 // that are each off by at most 2 ulp.  (The rounded division made the FFN 3 to 14 %
-// slower; a bare ex2.approx saves 1 % but is off by 50 ulp at g = -80, where its
+// slower; a bare ex2.approx saves 1 % but is off by 28 ulp near g = -80, where its
 // argument is rounded.)  Below g = -87.3 the division gives 0, as silu does to 1e-36.
 __device__ __forceinline__ float f8_silu_mul(float g, float u) {
   return __fmul_rn(__fdividef(g, 1.f + expf(-g)), u);

@@ -361,7 +361,8 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T* __restrict_
 // 128 x 128 blocks: a thread block keeps one tile in registers, in its own type,
 // between reading it and writing its codes; other blocks of the SM read meanwhile.
 // 16-byte bf16 accesses (V = 8): four blocks of 256 threads, 8 x 14336 x 4096 in
-// 204 us (6.9 TB/s; 5 blocks 208, 6 283, 3 217, two of 512 threads 272).  Otherwise two
+// 204 us (6.9 TB/s; 5 blocks 208, 6 283, 3 217, two of 512 threads 272; 217 us on the
+// slowest GPU it ran on).  Otherwise two
 // blocks of 512, whose tiles need as many registers (8 x 7168 x 2048 fp32 103 us,
 // 5.7 TB/s; four of 256 125).
 template <int V>
